@@ -751,9 +751,11 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = max3f(sv[e], sv[8 + e], sv[16 + e]);
 #pragma unroll
-      for (int j = 24; j < 64; j += 16)
+      for (int j = 24; j < 56; j += 16)
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = max3f(t[e], sv[j + e], sv[j + 8 + e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], sv[56 + e]);
       return max3f(max3f(t[0], t[1], t[2]), max3f(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
     };
     // P = 2^(s * scale * log2 e - m_ref) for one key half, stored as 32
