@@ -1,7 +1,9 @@
 /*
  * swa.h -- C ABI of libswa.so: sliding-window attention (SWA) on NVIDIA
  * B200 (sm_100a): forward (also over a per-layer schedule), backward,
- * ring-buffer and paged-cache decode, and chunked append into a ring.
+ * ring-buffer and paged-cache decode, and chunked append into a ring; with
+ * shaped scores and packed documents (forward, backward), rotated append into
+ * a paged cache, and decode behind a shared prefix.
  *
  * Every call is asynchronous on the CUDA stream passed as `stream` (a
  * cudaStream_t as void*; NULL = the legacy default stream).  All pointers
@@ -376,6 +378,129 @@ SWA_API int swa_paged_window(int64_t pos, int W, int page_size, int64_t* first_p
 SWA_API int swa_append(const void* q, const void* k_new, const void* v_new, void* k_ring,
                        void* v_ring, void* out, float* lse, const int64_t* pos0, int B, int C,
                        int H, int Hkv, int D, int W, float scale, void* stream);
+
+/*
+ * swa_rope_append_paged -- new tokens enter the paged KV cache of
+ * swa_decode_paged, with the rotary position rotation applied on the way.
+ *   q [T, H, D], k and v [T, Hkv, D] bf16: T tokens of B sequences, one after
+ *          another; q_stride, k_stride, v_stride: elements between tokens (at
+ *          least the row's size, multiples of 8), so slices of one fused
+ *          projection can be passed as they are
+ *   cu     [B + 1] int32, device, ascending: sequence b has the tokens
+ *          cu[b] .. cu[b + 1] - 1 (possibly none)
+ *   pos0   [B] int64, device: position of its first token; negative: the
+ *          sequence is inactive, nothing of it is written
+ *   inv_freq [rot / 2] fp32, device: angle of pair i at position p is
+ *          p * inv_freq[i]; the first rot dimensions of a head are rotated,
+ *          the others copied (rot a multiple of 16, 16 .. D)
+ *   interleaved: 0 rotates the pairs (i, i + rot / 2), 1 the pairs (2i, 2i + 1)
+ *   q_out  [T, H, D] bf16 with q_out_stride elements between tokens: the
+ *          rotated queries (may be q itself, with the same stride); rows of
+ *          tokens of no sequence are left as they are
+ *   k_pages, v_pages, block_table: as for swa_decode_paged; token t goes to
+ *          the row of its position.  Positions whose page is missing (an entry
+ *          outside [0, num_pages), or past max_pages) are not stored.
+ * Angles are formed in fp64 and reduced to one turn, then sin and cos in fp32;
+ * the rotation is fp32, rounded once to bf16.  D in {64, 128}; any page_size.
+ * T == 0 or B == 0 is a no-op.  One launch, no workspace.
+ */
+SWA_API int swa_rope_append_paged(const void* q, const void* k, const void* v, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, const float* inv_freq,
+                                  int rot, int interleaved, const int32_t* cu,
+                                  const int64_t* pos0, const int32_t* block_table, void* q_out,
+                                  int64_t q_out_stride, void* k_pages, void* v_pages, int T,
+                                  int B, int H, int Hkv, int D, int page_size, int num_pages,
+                                  int max_pages, void* stream);
+
+/*
+ * What shapes the scores of swa_forward_scored and swa_backward_scored beyond
+ * the window.  All pointers are device memory; zero / NULL leaves a part out.
+ *   softcap   > 0: scores become softcap * tanh(s / softcap)
+ *   slopes    [H] fp32: then slopes[h] * |i - j| is subtracted (distance bias)
+ *   cu_docs   [B, n_docs + 1] int32, ascending in [0, N]: row b of the batch
+ *             packs the documents [cu_docs[b][m], cu_docs[b][m + 1]); a token
+ *             sees keys of its own document only, and tokens before the first
+ *             and from the last boundary on are padding
+ *   prefix    [B, n_docs] int32 (needs cu_docs): the first prefix[b][m] tokens
+ *             of a document see each other in both directions (within
+ *             win_left)
+ */
+typedef struct swa_score {
+  float softcap;
+  const float* slopes;
+  const int32_t* cu_docs;
+  const int32_t* prefix;
+  int n_docs;
+} swa_score;
+
+/*
+ * swa_forward_scored -- swa_forward (dilation 1, no global tokens) with shaped
+ * scores: for row i of the document [ds, de) with prefix end pe,
+ *   K(i) = [max(ds, i - win_left), min(de - 1, max(i + win_right, pe - 1))],
+ *   s_ij = softcap tanh(scale q_i . k_j / softcap) - slopes[h] |i - j|.
+ * (win_left, win_right < 0: unbounded.)  Padding rows get out = 0 and lse =
+ * -inf; what q, k, v hold there, NaN included, reaches no other row.  score
+ * NULL: plain scores.  0 <= softcap <= 1e30.  Any GQA group.  Otherwise as
+ * swa_forward; no workspace.
+ */
+SWA_API int swa_forward_scored(const void* q, const void* k, const void* v, void* out,
+                               float* lse, int B, int H, int Hkv, int N, int D, int win_left,
+                               int win_right, const swa_score* score, float scale,
+                               void* stream);
+
+/*
+ * swa_backward_scored -- gradients of swa_forward_scored with respect to q, k
+ * and v: with t = tanh(scale q . k / softcap), P = exp(s - lse),
+ *   dV_j = sum_i P_ij dO_i,
+ *   dS_ij = P_ij (dO_i . v_j - dO_i . out_i) (1 - t_ij^2),
+ *   dQ_i = scale sum_j dS_ij k_j,  dK_j = scale sum_i dS_ij q_i.
+ * Tensors as for swa_backward; padding rows of dq, dk, dv are written as 0.
+ * delta: [B, H, N] fp32 device scratch of the caller (dO . out), overwritten;
+ * two calls may run at the same time if theirs differ.  No atomics: the same
+ * inputs give the same bits.
+ */
+SWA_API int swa_backward_scored(const void* q, const void* k, const void* v, const void* out,
+                                const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                                float* delta, int B, int H, int Hkv, int N, int D, int win_left,
+                                int win_right, const swa_score* score, float scale,
+                                void* stream);
+
+/*
+ * swa_decode_shared -- swa_decode_paged for a batch whose sequences begin with
+ * the same n_prefix tokens, whose pages are read once for all of them.
+ *   prefix_table [ceil(n_prefix / page_size)] int32, device: pages of the
+ *             positions 0 .. n_prefix - 1
+ *   block_table  [B, max_pages] int32, device: pages of the positions >=
+ *             n_prefix of each sequence (entries of earlier pages are not
+ *             read; a prefix that ends inside a page leaves the rest of that
+ *             logical page to the sequence's own page)
+ *   pos       [B] int64, device: position p of the new token; negative: the
+ *             sequence is inactive, out = 0 and lse = -inf
+ * The query sees the prefix positions j <= p (keep_prefix 0: only those of its
+ * window, j > p - W) and its own positions max(n_prefix, p - W + 1) .. p that
+ * the block table covers (pages outside the pool read as zero keys), with
+ *   s = softcap tanh(scale q . k / softcap) - slopes[h] (p - j)
+ * (softcap 0, slopes NULL: left out; slopes [H] fp32, device).  n_prefix 0
+ * gives a paged decode with these scores.  max_tail: the largest p - n_prefix
+ * + 1, or a guess (it only sets how the work is split).
+ * workspace: swa_decode_shared_workspace_bytes(...) bytes of the caller's
+ * device memory, 16-byte aligned, overwritten; two calls may run at the same
+ * time if theirs differ.  Nothing is allocated.  D in {64, 128}; H / Hkv <= 8;
+ * page_size a multiple of 64; num_pages * page_size < 2^31.  Rows of the pool
+ * that the query does not see may hold anything.
+ */
+SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_pages, void* out,
+                              float* lse, const int32_t* prefix_table, int n_prefix,
+                              const int32_t* block_table, const int64_t* pos, int B, int H,
+                              int Hkv, int D, int page_size, int num_pages, int max_pages, int W,
+                              int keep_prefix, int max_tail, float softcap, const float* slopes,
+                              float scale, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* swa_decode_shared_workspace_bytes -- workspace of swa_decode_shared for these
+   sizes on the calling thread's current device (0 for sizes it refuses). */
+SWA_API size_t swa_decode_shared_workspace_bytes(int B, int H, int Hkv, int D, int n_prefix,
+                                                 int W, int max_tail);
 
 /*
  * swa_device_error -- synchronises `stream`, then reports (and clears) a

@@ -19,19 +19,24 @@ _EXPORTS = (
     "library_path",
     "swa_append",
     "swa_backward",
+    "swa_backward_scored",
     "swa_decode",
     "swa_decode_ex",
     "swa_decode_noalloc",
     "swa_decode_noalloc_scratch_bytes",
     "swa_decode_paged",
+    "swa_decode_shared",
+    "swa_decode_shared_workspace_bytes",
     "swa_device_error",
     "swa_forward",
     "swa_forward_ex",
     "swa_forward_f32",
     "swa_forward_host",
     "swa_forward_layers",
+    "swa_forward_scored",
     "swa_paged_window",
     "swa_release",
+    "swa_rope_append_paged",
     "swa_schedule",
     "swa_selftest_timeout",
     "swa_set_workspace_allocator",

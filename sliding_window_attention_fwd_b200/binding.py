@@ -1,6 +1,7 @@
 """ctypes marshalling between torch tensors and the C ABI of libswa.so."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -35,6 +36,14 @@ _lib.swa_decode_noalloc_scratch_bytes.restype = ctypes.c_size_t
 _lib.swa_decode_paged.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                   _F, _P]
 _lib.swa_paged_window.argtypes = [ctypes.c_int64, _I, _I, _P, _P]
+_lib.swa_rope_append_paged.argtypes = ([_P] * 3 + [ctypes.c_int64] * 3 + [_P, _I, _I] + [_P] * 4
+                                       + [ctypes.c_int64, _P, _P] + [_I] * 8 + [_P])
+_lib.swa_forward_scored.argtypes = [_P] * 5 + [_I] * 7 + [_P, _F, _P]
+_lib.swa_backward_scored.argtypes = [_P] * 10 + [_I] * 7 + [_P, _F, _P]
+_lib.swa_decode_shared.argtypes = ([_P] * 6 + [_I, _P, _P] + [_I] * 10 + [_F, _P, _F, _P,
+                                                                          ctypes.c_size_t, _P])
+_lib.swa_decode_shared_workspace_bytes.argtypes = [_I] * 7
+_lib.swa_decode_shared_workspace_bytes.restype = ctypes.c_size_t
 _lib.swa_append.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]
 
 
@@ -57,6 +66,11 @@ class SwaLayer(ctypes.Structure):
                 ("global_idx", _P), ("n_global", _I), ("scale", _F)]
 
 
+class SwaScore(ctypes.Structure):
+    """struct swa_score of include/swa.h."""
+    _fields_ = [("softcap", _F), ("slopes", _P), ("cu_docs", _P), ("prefix", _P), ("n_docs", _I)]
+
+
 _lib.swa_forward_layers.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _P]
 _lib.swa_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                               _I, _P, _I, _F, _P]
@@ -73,7 +87,8 @@ _lib.swa_status_string.restype = ctypes.c_char_p
 _lib.swa_version.argtypes = []
 for _fn in ("swa_forward", "swa_forward_ex", "swa_forward_f32", "swa_decode", "swa_decode_ex",
             "swa_decode_paged", "swa_paged_window", "swa_append", "swa_forward_layers",
-            "swa_backward",
+            "swa_backward", "swa_rope_append_paged", "swa_forward_scored", "swa_backward_scored",
+            "swa_decode_shared",
             "swa_device_error", "swa_selftest_timeout", "swa_schedule", "swa_release",
             "swa_version"):
     getattr(_lib, _fn).restype = _I
@@ -423,6 +438,197 @@ def swa_append(q, k_new, v_new, k_ring, v_ring, pos0, out=None, lse=None, scale=
         _check(_lib.swa_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_ring), _ptr(v_ring),
                                _ptr(out), _ptr(lse), _ptr(pos0), B, C, H, Hkv, D, W,
                                float(scale), _stream(stream)), "swa_append")
+    return out
+
+
+def _score(q, softcap, slopes, cu_docs, prefix):
+    """The swa_score block of a call on q [B, N, H, D]."""
+    B, _, H, _ = q.shape
+    n = 0
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, 1, (H,))
+    if cu_docs is not None:
+        _need(cu_docs, "cu_docs", torch.int32, 2)
+        n = cu_docs.shape[1] - 1
+        if cu_docs.shape[0] != B or n < 1:
+            raise ValueError(f"cu_docs: expected [{B}, documents + 1], got {tuple(cu_docs.shape)}")
+    if prefix is not None:
+        if cu_docs is None:
+            raise ValueError("prefix needs cu_docs")
+        _need(prefix, "prefix", torch.int32, 2, (B, n))
+    _placed(q, slopes=slopes, cu_docs=cu_docs, prefix=prefix)
+    return SwaScore(float(softcap), None if slopes is None else slopes.data_ptr(),
+                    None if cu_docs is None else cu_docs.data_ptr(),
+                    None if prefix is None else prefix.data_ptr(), n)
+
+
+def _on_stream(stream):
+    """Context in which torch allocates for `stream` (as _stream takes it)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def swa_forward_scored(q, k, v, out=None, lse=None, win_left=-1, win_right=-1, softcap=0.0,
+                       slopes=None, cu_docs=None, prefix=None, scale=0.0, stream=None):
+    """bf16 forward with shaped scores (C: swa_forward_scored): tanh cap, distance
+    bias slopes [H] fp32, packed documents cu_docs [B, n + 1] int32 with prefix
+    lengths [B, n] int32.  Returns out."""
+    B, N, H, Hkv, D, out, _, _ = _fwd_common(q, k, v, out, lse, None, torch.bfloat16)
+    sc = _score(q, softcap, slopes, cu_docs, prefix)
+    if B == 0 or N == 0:
+        return out
+    with torch.cuda.device(q.device):
+        _check(_lib.swa_forward_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, Hkv,
+                                       N, D, int(win_left), int(win_right),
+                                       ctypes.c_void_p(ctypes.addressof(sc)), float(scale),
+                                       _stream(stream)), "swa_forward_scored")
+    return out
+
+
+def swa_backward_scored(q, k, v, out, dout, lse, win_left=-1, win_right=-1, softcap=0.0,
+                        slopes=None, cu_docs=None, prefix=None, scale=0.0, dq=None, dk=None,
+                        dv=None, stream=None):
+    """Gradients (dq, dk, dv) of swa_forward_scored (C: swa_backward_scored); out
+    and lse are the forward's outputs for the same arguments."""
+    if out is None or lse is None:
+        raise ValueError("out and lse (from the forward) are required")
+    _need(dout, "dout", torch.bfloat16, 4, q.shape)
+    B, N, H, Hkv, D, out, _, _ = _fwd_common(q, k, v, out, lse, None, torch.bfloat16)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for t, n, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        _need(t, n, torch.bfloat16, 4, ref.shape)
+    sc = _score(q, softcap, slopes, cu_docs, prefix)
+    _placed(q, dout=dout, dq=dq, dk=dk, dv=dv)
+    if B == 0 or N == 0:
+        return dq, dk, dv
+    with torch.cuda.device(q.device):
+        with _on_stream(stream):
+            delta = torch.empty(B * H * N, dtype=torch.float32, device=q.device)
+        _check(_lib.swa_backward_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout),
+                                        _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(delta), B,
+                                        H, Hkv, N, D, int(win_left), int(win_right),
+                                        ctypes.c_void_p(ctypes.addressof(sc)), float(scale),
+                                        _stream(stream)), "swa_backward_scored")
+    return dq, dk, dv
+
+
+def _token_rows(t, name, ref):
+    """t [T, heads, D]: dense rows, any stride between tokens -> that stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.device != ref.device:
+        raise ValueError(f"{name}: on {t.device}, expected {ref.device} like the queries")
+    T, heads, D = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the rows of a token must be contiguous")
+    if T > 1 and t.stride(0) < heads * D:
+        raise ValueError(f"{name}: tokens overlap")
+    return t.stride(0) if T > 1 else heads * D
+
+
+def swa_rope_append_paged(q, k, v, inv_freq, cu, pos0, block_table, k_pages, v_pages, page_size,
+                          q_out=None, interleaved=False, stream=None):
+    """New tokens enter a paged KV cache, rotated on the way (C:
+    swa_rope_append_paged).  q [T, H, D], k and v [T, Hkv, D] (any stride between
+    tokens); inv_freq [rot / 2] fp32; cu [B + 1] int32; pos0 [B] int64;
+    block_table [B, max_pages] int32; k_pages/v_pages [num_pages * page_size, Hkv,
+    D], updated in place.  Returns q_out [T, H, D], the rotated queries."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, n, torch.bfloat16, 3)
+    _need(inv_freq, "inv_freq", torch.float32, 1)
+    _need(cu, "cu", torch.int32, 1)
+    _need(pos0, "pos0", torch.int64, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    T, H, D = q.shape
+    rows, Hkv = k_pages.shape[0], k_pages.shape[1]
+    B = pos0.shape[0]
+    if (k.shape != (T, Hkv, D) or v.shape != k.shape or k_pages.shape[2] != D
+            or v_pages.shape != k_pages.shape or cu.shape[0] != B + 1
+            or block_table.shape[0] != B or int(page_size) < 1 or rows % int(page_size) != 0):
+        raise ValueError("k/v [T, Hkv, D], k_pages/v_pages [num_pages * page_size, Hkv, D], "
+                         "cu [B + 1], pos0 [B], block_table [B, *]")
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    _need(q_out, "q_out", torch.bfloat16, 3, (T, H, D))
+    strides = [_token_rows(t, n, q) for t, n in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"))]
+    _placed(q, inv_freq=inv_freq, cu=cu, pos0=pos0, block_table=block_table, k_pages=k_pages,
+            v_pages=v_pages)
+    if T == 0 or B == 0:
+        return q_out  # (an empty tensor has no address to check)
+    with torch.cuda.device(q.device):
+        _check(_lib.swa_rope_append_paged(_ptr(q), _ptr(k), _ptr(v), strides[0], strides[1],
+                                          strides[2], _ptr(inv_freq), 2 * inv_freq.shape[0],
+                                          int(bool(interleaved)), _ptr(cu), _ptr(pos0),
+                                          _ptr(block_table), _ptr(q_out), strides[3],
+                                          _ptr(k_pages), _ptr(v_pages), T, B, H, Hkv, D,
+                                          int(page_size), rows // int(page_size),
+                                          block_table.shape[1], _stream(stream)),
+               "swa_rope_append_paged")
+    return q_out
+
+
+def swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail) -> int:
+    """Bytes of workspace swa_decode_shared takes for these sizes (C:
+    swa_decode_shared_workspace_bytes)."""
+    return int(_lib.swa_decode_shared_workspace_bytes(int(B), int(H), int(Hkv), int(D),
+                                                      int(n_prefix), int(W), int(max_tail)))
+
+
+def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, pos, page_size, W,
+                      out=None, lse=None, keep_prefix=True, max_tail=None, softcap=0.0,
+                      slopes=None, scale=0.0, stream=None):
+    """Paged decode of a batch whose sequences begin with the same n_prefix tokens
+    (C: swa_decode_shared).  prefix_table [ceil(n_prefix / page_size)] int32;
+    block_table [B, max_pages] int32; keep_prefix: the prefix stays visible
+    behind the window W; max_tail: the longest sequence's tokens behind the
+    prefix (default: what the block table has room for), which only sets how
+    the work is split.  The workspace comes from torch's allocator.  Returns out
+    [B, H, D]."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_pages, "k_pages", torch.bfloat16, 3)
+    _need(v_pages, "v_pages", torch.bfloat16, 3)
+    _need(prefix_table, "prefix_table", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(pos, "pos", torch.int64, 1)
+    B, H, D = q.shape
+    rows, Hkv = k_pages.shape[0], k_pages.shape[1]
+    n_prefix, page_size = int(n_prefix), int(page_size)
+    if (k_pages.shape[2] != D or v_pages.shape != k_pages.shape or pos.shape != (B,)
+            or block_table.shape[0] != B or page_size < 1 or rows % page_size != 0):
+        raise ValueError("k_pages/v_pages [num_pages * page_size, Hkv, D], block_table [B, *], "
+                         "pos [B]")
+    if n_prefix < 0 or prefix_table.shape[0] * page_size < n_prefix:
+        raise ValueError("prefix_table: expected the pages of n_prefix >= 0 positions")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, 3, (B, H, D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2, (B, H))
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, 1, (H,))
+    _placed(q, q=q, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table,
+            block_table=block_table, pos=pos, out=out, lse=lse, slopes=slopes)
+    if B == 0:
+        return out
+    if max_tail is None:
+        max_tail = max(0, block_table.shape[1] * page_size - n_prefix)
+    max_tail = max(0, min(int(max_tail), 2 ** 31 - 1))
+    with torch.cuda.device(q.device):
+        nbytes = _lib.swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, int(W), max_tail)
+        with _on_stream(stream):
+            ws = torch.empty(max(16, nbytes), dtype=torch.uint8, device=q.device)
+        _check(_lib.swa_decode_shared(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse),
+                                      _ptr(prefix_table) if n_prefix else None, n_prefix,
+                                      _ptr(block_table), _ptr(pos), B, H, Hkv, D, page_size,
+                                      rows // page_size, block_table.shape[1], int(W),
+                                      int(bool(keep_prefix)), max_tail, float(softcap),
+                                      _ptr(slopes), float(scale), _ptr(ws), ws.numel(),
+                                      _stream(stream)), "swa_decode_shared")
     return out
 
 

@@ -42,6 +42,7 @@
 #include "swa_internal.h"
 #include "swa_ptx.cuh"
 #include "swa_sched.cuh"
+#include "swa_score.cuh"
 
 namespace swa {
 namespace {
@@ -92,6 +93,12 @@ struct BwdTcParams {
   int tile_prefix[kMaxClassesB + 1];  // 128-row tiles per class, prefix sums
   int Mv[kMaxClassesB];
   float scale, scale_log2;
+  // shaped scores (swa_score.cuh), fields as in the forward
+  float cap_in, cap_out;
+  const float* slopes;
+  const int32_t* cu_docs;
+  const int32_t* doc_pre;
+  int n_docs;
 };
 
 template <int D>
@@ -143,8 +150,55 @@ __device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
   return make_float2(ex2_approx(x.x), ex2_approx(x.y));
 }
 
-// ======================================================== dq kernel
+// Shaped scores of 32 raw products: x = cap(scale qk) - slope |i - j| - lse,
+// all in log2 units, and fac = 1 - tanh^2, the cap's derivative (1 without a
+// cap).  d0 + dj: signed distance of the first of the 32 and its step (+-1).
+struct Shape {
+  float cap_in, cap_out, scale_log2, nslope2;  // nslope2 0: no bias
+  // u values of the chunk -> whether all lie in the polynomial's range, for
+  // the whole warp
+  __device__ __forceinline__ bool small(const uint32_t (&sv)[32]) const {
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], fabsf(__uint_as_float(sv[e])));
+    const float m = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    return !__any_sync(0xffffffffu, m * cap_in > 1.f);
+  }
+  __device__ __forceinline__ float2 pair(float a, float b, bool poly, float dist0, float dist1,
+                                         float2 nlse, float2* fac) const {
+    float2 x;
+    if (cap_in > 0.f) {
+      const float2 u = mul2(make_float2(a, b), make_float2(cap_in, cap_in));
+      const float2 t = poly ? tanh_poly2(u) : make_float2(tanh_any(u.x), tanh_any(u.y));
+      x = fma2(t, make_float2(cap_out, cap_out), nlse);
+      *fac = fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
+    } else {
+      x = fma2(make_float2(a, b), make_float2(scale_log2, scale_log2), nlse);
+      *fac = make_float2(1.f, 1.f);
+    }
+    if (nslope2 != 0.f) {
+      x.x = fmaf(nslope2, fabsf(dist0), x.x);
+      x.y = fmaf(nslope2, fabsf(dist1), x.y);
+    }
+    return x;
+  }
+};
+
+// Zeros over the rows of a 128-row tile outside [z0, z1) (thread r: row r of
+// the tile at row0): padding may hold anything, and a product with P = 0 or
+// dS = 0 would keep its NaN.
 template <int D>
+__device__ __forceinline__ void clear_row(uint8_t* tile, int r, int row0, int z0, int z1) {
+  if (row0 + r >= z0 && row0 + r < z1) return;
+#pragma unroll 1
+  for (int i = 0; i < D / 8; ++i)
+    *reinterpret_cast<uint4*>(tile + (i / 8) * kChunkB + r * 128 + (i % 8) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ======================================================== dq kernel
+// kShaped: shaped scores and documents (token-level band, no dilation).
+template <int D, bool kShaped>
 __global__ void __launch_bounds__(kThreadsB, 1)
     swa_bwd_dq_kernel(const __grid_constant__ BwdTcParams p) {
   using C = BCfg<D>;
@@ -180,7 +234,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int g_kv = h / p.grp;
   const Geometry geo = make_geometry(p.N, p.L, p.R, p.d, p.bs);
   const int Mv = p.Mv[cl];
-  const TileRange tr = tile_range(geo, Mv, qt);
+  TileRange tr = tile_range(geo, Mv, qt);
+  DocTiles dt{};
+  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  if (kShaped) {
+    dt = doc_tiles<false>(dm, qt * kTileM, min(qt * kTileM + kTileM, Mv) - 1);
+    tr.kv_begin = dt.begin;
+    tr.kv_end = dt.end;
+  }
   const int n_tiles = tr.kv_end - tr.kv_begin;
   const int map_idx = p.bs > 1 ? 0 : cl;
 
@@ -214,7 +277,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 
   if (warp == 0) {
     // ============================== producer ==============================
-    if (lane == 0) {
+    if (lane == 0 && (!kShaped || n_tiles > 0)) {
       prefetch_tensormap(&p.tmQ[map_idx]);
       prefetch_tensormap(&p.tmDO[map_idx]);
       prefetch_tensormap(&p.tmK[map_idx]);
@@ -313,11 +376,22 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int m_v = qt * kTileM + r;
     const bool row_valid = m_v < Mv;
     const int i_phys = (int)phys_row(geo, c, m_v);
-    const int klo = key_lo(geo, m_v);
-    const int khi = key_hi(geo, m_v, Mv);
+    int klo = key_lo(geo, m_v);
+    int khi = key_hi(geo, m_v, Mv);
     int int_lo, int_hi;
     interior_tiles(geo, Mv, qt, &int_lo, &int_hi);
     const float sl2 = p.scale_log2;
+    bool real_row = row_valid;  // a row of some document
+    Shape shp{p.cap_in, p.cap_out, p.scale_log2, 0.f};
+    if (kShaped) {
+      const DocSpan ds = dm.of_thread(m_v, dt.mlo, dt.mhi);
+      real_row = row_valid && ds.start < ds.end;
+      klo = real_row ? dm.key_first(ds, m_v) : 1;
+      khi = real_row ? dm.key_last(ds, m_v) : 0;
+      int_lo = dt.int_lo;
+      int_hi = dt.int_hi;
+      if (p.slopes) shp.nslope2 = -__ldg(p.slopes + h) * kLog2e;
+    }
     // Delta_i = dO_i . out_i (each group sums a quarter of the row, the
     // parts meet in shared memory) and lse in log2 units; rows past the
     // class end get P = 0
@@ -325,7 +399,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     {
       float* part = reinterpret_cast<float*>(smem + C::kVec);  // [group][128]
       float acc0 = 0.f, acc1 = 0.f;
-      if (row_valid) {
+      if (real_row) {
         const size_t row = ((size_t)b * p.N + i_phys) * p.H + h;
         const uint4* a = reinterpret_cast<const uint4*>(p.dout + row * D);
         const uint4* o = reinterpret_cast<const uint4*>(p.out + row * D);
@@ -348,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       for (int g2 = 0; g2 < kGroupsB; ++g2) delta += part[g2 * kTileM + r];
       if (row_valid) {
         const size_t li = ((size_t)b * p.H + h) * p.N + i_phys;
-        lse2 = __ldg(p.lse + li) * kLog2e;
+        if (real_row) lse2 = __ldg(p.lse + li) * kLog2e;
         if (cg == 0) p.delta[li] = delta;
       }
     }
@@ -373,16 +447,41 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld32(tS + 32 * ch, sv);
         tmem_wait_ld();
         const int n0 = t * kTileN + 32 * ch;
+        const bool poly = kShaped && p.cap_in > 0.f && shp.small(sv);
+        const float d0 = kShaped ? (float)(m_v - n0) : 0.f;  // distance to the chunk's first key
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
-                           make_float2(sl2, sl2), make_float2(-lse2, -lse2));
+          float2 xs, fac;
+          if (kShaped)
+            xs = shp.pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]), poly,
+                          d0 - (float)(2 * e), d0 - (float)(2 * e + 1),
+                          make_float2(-lse2, -lse2), &fac);
+          else
+            xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
+                      make_float2(sl2, sl2), make_float2(-lse2, -lse2));
           if (edge) {
             const int j0 = n0 + 2 * e;
             if (!(j0 >= klo && j0 <= khi && j0 < Mv)) xs.x = -INFINITY;
             if (!(j0 + 1 >= klo && j0 + 1 <= khi && j0 + 1 < Mv)) xs.y = -INFINITY;
           }
           pr[i][e] = exp2_pair(xs, (e & 1) != 0 && !edge);
+          if (kShaped && p.cap_in > 0.f) {
+            // a masked score may be NaN: its factor must not meet P = 0
+            const float2 f = mul2(pr[i][e], fac);
+            pr[i][e] = make_float2(edge && pr[i][e].x == 0.f ? 0.f : f.x,
+                                   edge && pr[i][e].y == 0.f ? 0.f : f.y);
+          }
+        }
+      }
+      if (kShaped && cg == 0 && (t * kTileN < dt.c0 || t * kTileN + kTileN > dt.cn)) {
+        // S is computed: padding rows of K become zeros before dS K
+        const int st = it % S_;
+        w = mbar_wait(&full_k[st], (uint32_t)(it / S_) & 1u, p.err, abort_flag);
+        if (w) clear_row<D>(smem + C::kRing + st * C::kStageBytes, r, t * kTileN, dt.c0, dt.cn);
+        fence_proxy_async_smem();
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
         }
       }
       // then dS = P (dP - Delta)
@@ -402,8 +501,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
-                                                            __uint_as_float(dpv[2 * e + 1])), ndl));
+          float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
+                                                      __uint_as_float(dpv[2 * e + 1])), ndl));
+          if (kShaped && edge)
+            ds = make_float2(pr[i][e].x == 0.f ? 0.f : ds.x, pr[i][e].y == 0.f ? 0.f : ds.y);
           pk[e] = pack_bf16x2(ds.x, ds.y);
         }
         // dS of these 32 keys over the group's own (already read) S columns
@@ -458,7 +559,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 }
 
 // ======================================================== dk / dv kernel
-template <int D>
+template <int D, bool kShaped>
 __global__ void __launch_bounds__(kThreadsB, 1)
     swa_bwd_dkdv_kernel(const __grid_constant__ BwdTcParams p) {
   using C = BCfg<D>;
@@ -493,7 +594,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int c = p.class0 + cl;
   const Geometry geo = make_geometry(p.N, p.L, p.R, p.d, p.bs);
   const int Mv = p.Mv[cl];
-  const TileRange qr = qtile_range_keys(geo, Mv, kt * kTileN);
+  TileRange qr = qtile_range_keys(geo, Mv, kt * kTileN);
+  DocTiles dt{};
+  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  if (kShaped) {
+    dt = doc_tiles<true>(dm, kt * kTileN, min(kt * kTileN + kTileN, Mv) - 1);
+    qr.kv_begin = dt.begin;
+    qr.kv_end = dt.end;
+  }
   const int grp = p.grp;
   const int n_steps = (qr.kv_end - qr.kv_begin) * grp;  // (query tile, head of the group)
   const int map_idx = p.bs > 1 ? 0 : cl;
@@ -526,7 +636,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 
   if (warp == 0) {
     // ============================== producer ==============================
-    if (lane == 0) {
+    if (lane == 0 && (!kShaped || n_steps > 0)) {
       prefetch_tensormap(&p.tmQ[map_idx]);
       prefetch_tensormap(&p.tmDO[map_idx]);
       prefetch_tensormap(&p.tmK[map_idx]);
@@ -550,7 +660,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const int m = qt * kTileM + lane + 32 * u;
         l2[u] = INFINITY;
         dl[u] = 0.f;
-        if (m < Mv) {
+        if (m < Mv && (!kShaped || (m >= dt.c0 && m < dt.cn))) {
           const size_t li = ((size_t)b * p.H + h) * p.N + phys_row(geo, c, m);
           l2[u] = __ldg(p.lse + li) * kLog2e;
           dl[u] = p.delta[li];
@@ -572,7 +682,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       mbar_arrive(&full[st]);
       last = s;
     }
-    if (lane == 0 && *abort_flag) {  // leave no copy writing shared memory behind
+    if (lane == 0 && *abort_flag && (!kShaped || n_steps > 0)) {
+      // leave no copy writing shared memory behind
       drain_copies(full_kv, 1, 0, 0);
       drain_copies(full, S_, 0, last);
     }
@@ -656,10 +767,21 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     int int_lo, int_hi;
     interior_qtiles_keys(geo, Mv, kt * kTileN, &int_lo, &int_hi);
     const float sl2 = p.scale_log2;
+    Shape shp{p.cap_in, p.cap_out, p.scale_log2, 0.f};
+    if (kShaped) {
+      const DocSpan ds = dm.of_thread(j_v, dt.mlo, dt.mhi);
+      const bool real_key = key_valid && ds.start < ds.end;
+      qlo = real_key ? dm.query_first(ds, j_v) : 1;
+      qhi = real_key ? dm.query_last(ds, j_v) : 0;
+      int_lo = dt.int_lo;
+      int_hi = dt.int_hi;
+    }
     bool ok = true;
     for (int s = 0; s < n_steps; ++s) {
       const int st = s % S_;
       const int qt = qr.kv_begin + s / grp;
+      if (kShaped && p.slopes)
+        shp.nslope2 = -__ldg(p.slopes + g_kv * grp + s % grp) * kLog2e;
       const bool edge = !(qt >= int_lo && qt <= int_hi);
       // P^T as soon as S^T is in TMEM (dP^T is still being computed)
       bool w = mbar_wait(st_full, (uint32_t)s & 1u, p.err, abort_flag);
@@ -677,6 +799,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld32(tS + 32 * ch, sv);
         tmem_wait_ld();
         const int i0 = qt * kTileM + 32 * ch;
+        const bool poly = kShaped && p.cap_in > 0.f && shp.small(sv);
+        const float d0 = kShaped ? (float)(i0 - j_v) : 0.f;  // distance of the chunk's first row
         const float4* l4 = reinterpret_cast<const float4*>(vl + 32 * ch);
         uint32_t pp[16];
 #pragma unroll
@@ -686,19 +810,45 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int h2 = 0; h2 < 2; ++h2) {
             const int e = 2 * e2 + h2;
             const float2 lp = h2 ? make_float2(l.z, l.w) : make_float2(l.x, l.y);
-            float2 xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
-                             make_float2(sl2, sl2), make_float2(-lp.x, -lp.y));
+            float2 xs, fac;
+            if (kShaped)
+              xs = shp.pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]), poly,
+                            d0 + (float)(2 * e), d0 + (float)(2 * e + 1),
+                            make_float2(-lp.x, -lp.y), &fac);
+            else
+              xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
+                        make_float2(sl2, sl2), make_float2(-lp.x, -lp.y));
             if (edge) {
               if (!(i0 + 2 * e >= qlo && i0 + 2 * e <= qhi)) xs.x = -INFINITY;
               if (!(i0 + 2 * e + 1 >= qlo && i0 + 2 * e + 1 <= qhi)) xs.y = -INFINITY;
             }
             pr[i][e] = exp2_pair(xs, h2 != 0 && !edge);
             pp[e] = pack_bf16x2(pr[i][e].x, pr[i][e].y);
+            if (kShaped && p.cap_in > 0.f) {
+              const float2 f = mul2(pr[i][e], fac);
+              pr[i][e] = make_float2(edge && pr[i][e].x == 0.f ? 0.f : f.x,
+                                     edge && pr[i][e].y == 0.f ? 0.f : f.y);
+            }
           }
         }
         // P^T of these 32 query columns over the group's own (already read)
         // columns of S^T
         tmem_st16(tS + 32 * kCpg * cg + 16 * i, pp);
+      }
+      if (kShaped && cg == 0 && (qt * kTileM < dt.c0 || qt * kTileM + kTileM > dt.cn)) {
+        // S^T is computed: padding rows of Q and dO become zeros before dV and
+        // dK (dP^T may still be reading dO: only columns that are masked)
+        w = mbar_wait(&full[st], (uint32_t)(s / S_) & 1u, p.err, abort_flag);
+        if (w) {
+          uint8_t* qb = smem + C::kRing + st * C::kStageBytes;
+          clear_row<D>(qb, r, qt * kTileM, dt.c0, dt.cn);
+          clear_row<D>(qb + C::kTile, r, qt * kTileM, dt.c0, dt.cn);
+        }
+        fence_proxy_async_smem();
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
       }
       // P^T is complete: dV(s), then S^T(s + 1), may go while dS^T is formed
       tmem_wait_st();
@@ -726,8 +876,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int h2 = 0; h2 < 2; ++h2) {
             const int e = 2 * e2 + h2;
             const float2 dn = h2 ? make_float2(-dl.z, -dl.w) : make_float2(-dl.x, -dl.y);
-            const float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
-                                                              __uint_as_float(dpv[2 * e + 1])), dn));
+            float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
+                                                        __uint_as_float(dpv[2 * e + 1])), dn));
+            if (kShaped && edge)
+              ds = make_float2(pr[i][e].x == 0.f ? 0.f : ds.x, pr[i][e].y == 0.f ? 0.f : ds.y);
             pd[e] = pack_bf16x2(ds.x, ds.y);
           }
         }
@@ -784,15 +936,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
 }
 
-template <int D>
+template <int D, bool kShaped>
 int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* out,
                        const void* dout, const float* lse, void* dq, void* dk, void* dv,
                        float* delta, int B, int H, int Hkv, int N, int L, int R, int d, int bs,
-                       float scale, cudaStream_t stream) {
+                       float scale, cudaStream_t stream, const ScoreArgs* sc = nullptr) {
   using C = BCfg<D>;
   static std::atomic<unsigned long long> attr_dq{0}, attr_dkdv{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D>), C::kAlloc, attr_dq) ||
-      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D>), C::kAlloc,
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D, kShaped>), C::kAlloc, attr_dq) ||
+      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D, kShaped>), C::kAlloc,
                       attr_dkdv))
     return SWA_ERR_CUDA;
   int* err = device_error_word();
@@ -826,6 +978,16 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
       p.bs = geo.bs;
       p.scale = scale;
       p.scale_log2 = scale * kLog2e;
+      if (kShaped) {
+        if (sc->softcap > 0.f) {
+          p.cap_in = scale / sc->softcap;
+          p.cap_out = sc->softcap * kLog2e;
+        }
+        p.slopes = sc->slopes;
+        p.cu_docs = sc->cu_docs;
+        p.doc_pre = sc->prefix;
+        p.n_docs = sc->n_docs;
+      }
       p.tile_prefix[0] = 0;
       for (int cl = 0; cl < p.nclass; ++cl) {
         p.Mv[cl] = class_valid_rows(geo, c0 + cl);
@@ -863,12 +1025,12 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
         const long grid = ntiles * B * H;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
-        swa_bwd_dq_kernel<D><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
+        swa_bwd_dq_kernel<D, kShaped><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
       } else {
         const long grid = ntiles * B * Hkv;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
-        swa_bwd_dkdv_kernel<D><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
+        swa_bwd_dkdv_kernel<D, kShaped><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
       }
       if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
     }
@@ -883,11 +1045,27 @@ int launch_backward_tc(const void* q, const void* k, const void* v, const void* 
                        float* delta, int B, int H, int Hkv, int N, int D, int L, int R, int d,
                        int bs, float scale, cudaStream_t stream) {
   if (D == 128)
-    return launch_bwd_tc_impl<128>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L,
+    return launch_bwd_tc_impl<128, false>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L,
                                    R, d, bs, scale, stream);
   if (D == 64)
-    return launch_bwd_tc_impl<64>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, R,
+    return launch_bwd_tc_impl<64, false>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, R,
                                   d, bs, scale, stream);
+  return SWA_ERR_UNSUPPORTED;
+}
+
+int launch_bwd_scored(const void* q, const void* k, const void* v, const void* out,
+                      const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                      float* delta, int B, int H, int Hkv, int N, int D, int L, int R,
+                      const ScoreArgs& sc, float scale, cudaStream_t stream) {
+  if (sc.plain())
+    return launch_backward_tc(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, D, L, R,
+                              1, 0, scale, stream);
+  if (D == 128)
+    return launch_bwd_tc_impl<128, true>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N,
+                                         L, R, 1, 0, scale, stream, &sc);
+  if (D == 64)
+    return launch_bwd_tc_impl<64, true>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N,
+                                        L, R, 1, 0, scale, stream, &sc);
   return SWA_ERR_UNSUPPORTED;
 }
 

@@ -402,6 +402,164 @@ SWA_API int swa_append(const void* q, const void* k_new, const void* v_new, void
                        resolve_scale(scale, D), static_cast<cudaStream_t>(stream));
 }
 
+SWA_API int swa_rope_append_paged(const void* q, const void* k, const void* v, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, const float* inv_freq,
+                                  int rot, int interleaved, const int32_t* cu,
+                                  const int64_t* pos0, const int32_t* block_table, void* q_out,
+                                  int64_t q_out_stride, void* k_pages, void* v_pages, int T,
+                                  int B, int H, int Hkv, int D, int page_size, int num_pages,
+                                  int max_pages, void* stream) {
+  if (T < 0 || B < 0 || H <= 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 ||
+      max_pages <= 0 || rot < 0 || rot > D)
+    return SWA_ERR_ARG;
+  if (!q || !k || !v || !inv_freq || !cu || !pos0 || !block_table || !q_out || !k_pages ||
+      !v_pages)
+    return SWA_ERR_ARG;
+  const int64_t qrow = (int64_t)H * D, krow = (int64_t)Hkv * D;
+  if (q_stride < qrow || k_stride < krow || v_stride < krow || q_out_stride < qrow)
+    return SWA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(k_pages) || !aligned16(v_pages) || q_stride % 8 || k_stride % 8 ||
+      v_stride % 8 || q_out_stride % 8 || (reinterpret_cast<uintptr_t>(inv_freq) & 3u) ||
+      (reinterpret_cast<uintptr_t>(cu) & 3u) || (reinterpret_cast<uintptr_t>(pos0) & 7u) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u))
+    return SWA_ERR_ALIGN;
+  if ((D != 64 && D != 128) || rot % 16 != 0 || rot == 0) return SWA_ERR_UNSUPPORTED;
+  if (H > 4096 || Hkv > 4096) return SWA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return SWA_OK;
+  return launch_rope_append(q, k, v, q_stride, k_stride, v_stride, inv_freq, rot,
+                            interleaved != 0, cu, pos0, block_table, q_out, q_out_stride,
+                            k_pages, v_pages, T, B, H, Hkv, D, page_size, num_pages, max_pages,
+                            static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+int check_softcap(float softcap) {
+  return softcap >= 0.f && softcap <= 1e30f ? SWA_OK : SWA_ERR_ARG;  // (a NaN fails both)
+}
+
+int check_score(const swa_score* sc) {
+  if (!sc) return SWA_OK;
+  if (check_softcap(sc->softcap) != SWA_OK || sc->n_docs < 0) return SWA_ERR_ARG;
+  if ((sc->cu_docs != nullptr) != (sc->n_docs > 0)) return SWA_ERR_ARG;
+  if (sc->prefix && !sc->cu_docs) return SWA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(sc->slopes) & 3u) ||
+      (reinterpret_cast<uintptr_t>(sc->cu_docs) & 3u) ||
+      (reinterpret_cast<uintptr_t>(sc->prefix) & 3u))
+    return SWA_ERR_ALIGN;
+  return SWA_OK;
+}
+
+ScoreArgs score_args(const swa_score* sc) {
+  ScoreArgs a;
+  if (sc) {
+    a.softcap = sc->softcap;
+    a.slopes = sc->slopes;
+    a.cu_docs = sc->cu_docs;
+    a.prefix = sc->prefix;
+    a.n_docs = sc->n_docs;
+  }
+  return a;
+}
+}  // namespace
+
+SWA_API int swa_forward_scored(const void* q, const void* k, const void* v, void* out,
+                               float* lse, int B, int H, int Hkv, int N, int D, int win_left,
+                               int win_right, const swa_score* score, float scale,
+                               void* stream) {
+  int st = check_forward_bf16(q, k, v, out, lse, B, H, Hkv, N, D, 1, 0, nullptr, 0);
+  if (st != SWA_OK) return st;
+  st = check_score(score);
+  if (st != SWA_OK) return st;
+  if (B == 0 || N == 0) return SWA_OK;
+  return launch_fwd_scored(q, k, v, out, lse, B, H, Hkv, N, D, win_left, win_right,
+                           score_args(score), resolve_scale(scale, D),
+                           static_cast<cudaStream_t>(stream));
+}
+
+SWA_API int swa_backward_scored(const void* q, const void* k, const void* v, const void* out,
+                                const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                                float* delta, int B, int H, int Hkv, int N, int D, int win_left,
+                                int win_right, const swa_score* score, float scale,
+                                void* stream) {
+  int st = check_forward_bf16(q, k, v, const_cast<void*>(out), nullptr, B, H, Hkv, N, D, 1, 0,
+                              nullptr, 0);
+  if (st != SWA_OK) return st;
+  if (!dout || !lse || !dq || !dk || !dv || !delta) return SWA_ERR_ARG;
+  if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(delta) & 3u))
+    return SWA_ERR_ALIGN;
+  st = check_score(score);
+  if (st != SWA_OK) return st;
+  if (B == 0 || N == 0) return SWA_OK;
+  return launch_bwd_scored(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, D, win_left,
+                           win_right, score_args(score), resolve_scale(scale, D),
+                           static_cast<cudaStream_t>(stream));
+}
+
+SWA_API size_t swa_decode_shared_workspace_bytes(int B, int H, int Hkv, int D, int n_prefix,
+                                                 int W, int max_tail) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || D <= 0 || n_prefix < 0 || W <= 0 ||
+      max_tail < 0)
+    return 0;
+  return shared_plan(B, H, Hkv, D, n_prefix, W, max_tail).bytes;
+}
+
+SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_pages, void* out,
+                              float* lse, const int32_t* prefix_table, int n_prefix,
+                              const int32_t* block_table, const int64_t* pos, int B, int H,
+                              int Hkv, int D, int page_size, int num_pages, int max_pages, int W,
+                              int keep_prefix, int max_tail, float softcap, const float* slopes,
+                              float scale, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (B < 0 || H <= 0 || Hkv <= 0 || D <= 0 || W <= 0 || page_size <= 0 || num_pages <= 0 ||
+      max_pages <= 0 || n_prefix < 0 || max_tail < 0)
+    return SWA_ERR_ARG;
+  if (H % Hkv != 0 || check_softcap(softcap) != SWA_OK) return SWA_ERR_ARG;
+  if (!q || !k_pages || !v_pages || !out || !block_table || !pos || !workspace ||
+      (n_prefix > 0 && !prefix_table))
+    return SWA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(pos) & 7u) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(prefix_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
+    return SWA_ERR_ALIGN;
+  if (D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
+  // (rows of the pool are 32-bit coordinates of a TMA box)
+  if (H / Hkv > 8 || page_size % kBlockRows != 0 ||
+      (int64_t)num_pages * page_size > 0x7fffffffLL ||
+      (int64_t)B * (H / Hkv) > 0x7fffffffLL - 2 * kTileM || n_prefix > 0x7fffffff - 2 * kTileN)
+    return SWA_ERR_UNSUPPORTED;
+  if (B == 0) return SWA_OK;
+  const SharedPlan pl = shared_plan(B, H, Hkv, D, n_prefix, W, max_tail);
+  if (workspace_bytes < pl.bytes) return SWA_ERR_ARG;
+  SharedArgs a;
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.out = out;
+  a.lse = lse;
+  a.prefix_table = prefix_table;
+  a.table = block_table;
+  a.pos = pos;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.n_prefix = n_prefix;
+  a.W = W;
+  a.keep = keep_prefix != 0;
+  a.max_tail = max_tail;
+  a.scale = resolve_scale(scale, D);
+  a.softcap = softcap;
+  a.slopes = slopes;
+  return launch_decode_shared(a, pl, workspace, static_cast<cudaStream_t>(stream));
+}
+
 SWA_API int swa_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return SWA_ERR_CUDA;

@@ -55,6 +55,7 @@
 #include "swa_internal.h"
 #include "swa_ptx.cuh"
 #include "swa_sched.cuh"
+#include "swa_score.cuh"
 
 namespace swa {
 namespace {
@@ -132,6 +133,21 @@ struct FwdParams {
   uint4* v_ring;
   const uint4* kn_raw;
   const uint4* vn_raw;
+  // Shaped scores (swa_score.cuh): cap_in = scale / cap and cap_out = cap *
+  // log2 e (cap_in 0: no cap), slopes [H] (NULL: no bias), documents.
+  float cap_in, cap_out;
+  const float* slopes;
+  const int32_t* cu_docs;  // [B, n_docs + 1] (NULL: one document)
+  const int32_t* doc_pre;  // [B, n_docs] (NULL: no prefixes)
+  int n_docs;
+  // Shared prefix (decode): the keys are the N = n_prefix positions in the
+  // pages table[0 ..] of a pool (tmK[0] / tmV[0]: [pool rows, Hkv, D]); query
+  // row R of a kv head is its head R % grp of sequence R / grp, at position
+  // pos0[b]; it sees the prefix keys j <= pos0[b], and unless keep only those
+  // of its window, j > pos0[b] - win.  Split into nsplit parts like a query
+  // window, written to part_o [nsplit, B, H, D] / part_lse.
+  const int32_t* table;
+  int page_size, num_pages, keep;
 };
 
 template <int D, int NSLOT, int NSTREAM>
@@ -170,7 +186,8 @@ struct Cfg {
 
 // KIND (compile-time, so each form carries only its own code): 0 band (and
 // token/block dilation) only; 1 the query window of a chunked append; 2 the
-// band plus global tokens (global-key tiles and global query rows).
+// band plus global tokens (global-key tiles and global query rows); 3 the
+// band with shaped scores and documents; 4 the shared prefix of a decode.
 template <int D, int NSLOT, int NSTREAM, int KIND>
 __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
                                   Cfg<D, NSLOT, NSTREAM>::kMinBlocks)
@@ -211,19 +228,26 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   const int npair = stack ? p.H / (2 * NSLOT) : (p.H + NSLOT - 1) / NSLOT;
   int x = blockIdx.x;
   constexpr bool glob = KIND == 2;
+  constexpr bool docs = KIND == 3;
+  constexpr bool shared = KIND == 4;
+  constexpr bool scored = docs || shared;
   const bool gitem = glob && x < p.n_gitems;
   if (glob && !gitem) x -= p.n_gitems;
   int sp = 0;  // part of a split key walk
-  if (qwin) {
+  if (qwin || shared) {
     sp = x % p.nsplit;
     x /= p.nsplit;
   }
-  const int hp = x % npair;
-  x /= npair;
-  const int b = x % p.B;
-  x /= p.B;
+  const int hp = shared ? 0 : x % npair;
+  x /= shared ? 1 : npair;
+  const int g_kv = shared ? x % p.Hkv : 0;
+  x /= shared ? p.Hkv : 1;
+  const int b = shared ? 0 : x % p.B;
+  x /= shared ? 1 : p.B;
   int cl = 0, qt = 0, gq0 = 0, gcnt = 0;
-  if (gitem) {
+  const int sr0 = shared ? x * NSLOT * kTileM : 0;  // first query row of this item
+  if (shared) {
+  } else if (gitem) {
     gq0 = x * kTileM;  // first global row of this tile
     gcnt = min(kTileM, p.n_global - gq0);
   } else {
@@ -242,6 +266,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     slot_ok[s] = head[s] < p.H;
     if (!slot_ok[s]) head[s] = p.H - 1;
     kvh[s] = head[s] / grp;
+    if (shared) {
+      slot_ok[s] = sr0 + s * kTileM < p.B * grp;
+      kvh[s] = g_kv;
+    }
   }
   // in-place query window: per-batch key layout (see FwdParams::inplace)
   const bool inplace = qwin && p.inplace;
@@ -258,12 +286,44 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
                              : make_geometry(p.N, p.L, p.R, p.d, p.bs);
   // a global tile's keys are the physical rows of the sequence
   const int Mv = gitem ? p.N : (inplace ? ip_cs + p.Mq : p.Mv[cl]);
-  const int Mq = qwin ? p.Mq : Mv;           // query rows (local; stacked: tokens)
+  const int Mq = qwin ? p.Mq : (shared ? kTileM : Mv);  // query rows (local; stacked: tokens)
   const int q0 = qwin ? (inplace ? ip_cs : p.q0) : 0;  // virtual row of local query row 0
   const int qm0 = q0 + qt * kTileM;
   const int qm1 = q0 + min(qt * kTileM + kTileM - 1, Mq - 1);
   TileRange tr;
-  if (gitem) {
+  DocTiles dt{};
+  const DocMask dm{docs && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   docs && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  if (docs) {
+    dt = doc_tiles<false>(dm, qm0, qm1);
+    tr.kv_begin = dt.begin;
+    tr.kv_end = dt.end;
+  } else if (shared) {
+    // the tiles any of the item's rows sees: the sequences [b0, b1]
+    const int b0 = sr0 / grp, b1 = min(sr0 + NSLOT * kTileM, p.B * grp) - 1;
+    int lo = p.N, hi = -1;
+    for (int bb = b0 + lane; bb <= b1 / grp; bb += 32) {
+      const long long pb = p.pos0[bb];
+      if (pb < 0) continue;
+      const long long first = p.keep || pb < p.win ? 0 : pb - p.win + 1;
+      lo = first < lo ? (int)first : lo;
+      hi = max(hi, pb < p.N - 1 ? (int)pb : p.N - 1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    tr.kv_begin = lo / kTileN;
+    tr.kv_end = hi >= lo ? hi / kTileN + 1 : tr.kv_begin;
+    const int n = tr.kv_end - tr.kv_begin;
+    const int part = (n + p.nsplit - 1) / p.nsplit;
+    const int a = tr.kv_begin + sp * part;
+    const int z = tr.kv_end;
+    tr.kv_begin = min(a, z);
+    tr.kv_end = min(a + part, z);
+  } else if (gitem) {
     // every key tile (causal: up to the tile's last, i.e. largest, global row)
     int last = __ldg(p.G + gq0 + gcnt - 1);
     last = last < 0 ? 0 : (last >= p.N ? p.N - 1 : last);
@@ -318,6 +378,14 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   // the source of a 64-row key box at virtual row vrow (a multiple of 64):
   // its tensor map and row coordinate
   auto kv_box = [&](int kv, int vrow, int* row) -> const CUtensorMap* {
+    if (shared) {
+      // rows past the prefix, and pages outside the pool's, read as zeros
+      const int lp = vrow / p.page_size;
+      const int page = vrow < p.N ? __ldg(p.table + lp) : -1;
+      *row = page < 0 || page >= p.num_pages ? -kBlockRows
+                                             : page * p.page_size + vrow % p.page_size;
+      return kv ? &p.tmV[0] : &p.tmK[0];
+    }
     if (inplace) {
       if (vrow < ip_cs) {
         *row = (ip_base + vrow) % p.win;
@@ -406,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
         prefetch_tensormap(&p.tmKf);
         prefetch_tensormap(&p.tmVf);
       }
-      load_q();
+      if (!shared) load_q();
       for (int it = 0; it < n_early_k || it < n_early_v; ++it)
         for (int kv = 0; kv < 2; ++kv)
           if (it < (kv ? n_early_v : n_early_k) && !withheld(it, kv)) load_kv(it, kv);
@@ -415,6 +483,24 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
+  }
+  if (shared && n_tiles > 0 && threadIdx.x >= 128) {
+    // gather the item's query rows (zeros past the last) into the swizzled
+    // layout of a TMA box
+    constexpr int kC16 = D / 8;
+    for (int idx = (int)threadIdx.x - 128; idx < NSLOT * kTileM * kC16; idx += 128 * NSLOT) {
+      const int row = idx / kC16, c16 = idx % kC16;
+      const int R = sr0 + row;
+      uint4 val = make_uint4(0u, 0u, 0u, 0u);
+      if (R < p.B * grp)
+        val = __ldg(reinterpret_cast<const uint4*>(
+            p.q_raw + ((size_t)(R / grp) * p.H + (size_t)g_kv * grp + R % grp) * D + c16 * 8));
+      const int rr = row % kTileM;
+      uint8_t* d8 = smem + C::kQ + (row / kTileM) * C::kTile + (c16 / 8) * kChunkBytes + rr * 128 +
+                    (((c16 % 8) ^ (rr % 8)) * 16);
+      *reinterpret_cast<uint4*>(d8) = val;
+    }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -516,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 #else
         const int skip = -1;
 #endif
-        drain_copies(full_q, 1, 0, 0);
+        if (!shared) drain_copies(full_q, 1, 0, 0);
         drain_copies(full_k, kStages, 0, last_k, skip);
         drain_copies(full_v, kStages, 0, last_v);
       }
@@ -578,7 +664,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
                    (it > 0 || !early || kk > 0) ? 1u : 0u);
           }
         };
-        bool ok = mbar_wait(full_q, 0, p.err, abort_flag) &&
+        // (a shared prefix's query rows were in place at the block barrier)
+        bool ok = (shared || mbar_wait(full_q, 0, p.err, abort_flag)) &&
                   mbar_wait(&full_k[0], 0, p.err, abort_flag);
         tc_fence_after();
         if (ok) {
@@ -634,12 +721,26 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     const uint32_t tS = tmem + 128u * slot + lane_off;
     const uint32_t tO = tmem + C::kOcol + (uint32_t)D * slot + lane_off;
     // stacked: lanes 64-127 are the slot's second head, same tokens
-    const int h = head[slot] + (stack ? (r >> 6) : 0);
+    const int sR = sr0 + slot * kTileM + r;  // shared prefix: row among the kv head's queries
+    const int h = shared ? g_kv * grp + sR % grp : head[slot] + (stack ? (r >> 6) : 0);
     const int m_row = stack ? (r & 63) : qt * kTileM + r;  // local query row
     const int m_v = q0 + m_row;         // its virtual row among the keys
     bool row_valid;
     int klo, khi, i_phys;
-    if (gitem) {
+    long long pos_q = 0;  // position of the row's query (shared prefix)
+    if (shared) {
+      row_valid = sR < p.B * grp;
+      pos_q = row_valid ? p.pos0[sR / grp] : -1;
+      klo = p.keep || pos_q < p.win ? 0 : (int)min(pos_q - p.win + 1, (long long)p.N);
+      khi = pos_q < 0 ? -1 : (pos_q < p.N - 1 ? (int)pos_q : p.N - 1);
+      i_phys = 0;
+    } else if (docs) {
+      row_valid = m_row < Mq && slot_ok[slot];
+      const DocSpan ds = dm.of_thread(m_v, dt.mlo, dt.mhi);
+      klo = dm.key_first(ds, m_v);
+      khi = row_valid ? dm.key_last(ds, m_v) : -1;
+      i_phys = m_v;
+    } else if (gitem) {
       // global row: every key of the sequence (causal: up to the row)
       row_valid = r < gcnt && slot_ok[slot];
       int gv = r < gcnt ? __ldg(p.G + gq0 + r) : 0;
@@ -681,7 +782,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     const int ghi = p.R < 0 ? 0x40000000
                             : (block_mode ? (i_phys / p.bs + (p.R / p.bs) * p.d + 1) * p.bs - 1
                                           : i_phys + p.R * p.d);
-    const float sl2 = p.scale_log2;
+    // shaped scores are turned into log2 units as they are read (the cap and
+    // the bias are not linear in them): what follows then scales by 1
+    const bool cap_on = scored && p.cap_in > 0.f;
+    const bool bias_on = scored && p.slopes != nullptr;
+    const float nslope2 = bias_on ? -__ldg(p.slopes + h) * 1.4426950408889634f : 0.f;
+    const float sl2 = cap_on || bias_on ? 1.f : p.scale_log2;
     float m_used = -INFINITY;  // running max, scaled log2 units
     float l = 0.f;
     bool ok = slot_ok[slot];
@@ -692,9 +798,17 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     // last 128 rows below the last token)
     interior_tiles_rows(g, Mv, stack ? q0 + Mq - kTileM : qm0, &int_lo, &int_hi);
     const int last_row = stack ? Mq - 1 : qt * kTileM + kTileM - 1;  // local
+    if (docs) {
+      int_lo = dt.int_lo;
+      int_hi = dt.int_hi;
+    } else if (shared) {
+      // (klo differs between the rows: the warp's mask test sorts it out)
+      int_lo = (klo + kTileN - 1) / kTileN;
+      int_hi = (khi + 1) / kTileN - 1;
+    }
     // mask every tile: global tiles, rows of negative positions, partial
     // query tiles, and in-place windows that start in the chunk
-    if (gitem || lo_b > ip_hs || (stack ? Mq < 64 : qt * kTileM + kTileM > Mq) ||
+    if (gitem || lo_b > ip_hs || (!shared && (stack ? Mq < 64 : qt * kTileM + kTileM > Mq)) ||
         (inplace && last_row >= p.win - 1))
       int_hi = int_lo - 1;
 
@@ -708,6 +822,57 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
         for (int e = 0; e < 32; ++e) sv[jj * 32 + e] = __uint_as_float(v[e]);
       }
       tmem_wait_ld();
+    };
+    // cap and bias of the 64 scores of key half hf of tile it, into log2 units
+    auto shape_half = [&](int it, int hf, float (&sv)[64]) {
+      if (cap_on) {
+        const float2 ci = make_float2(p.cap_in, p.cap_in), co = make_float2(p.cap_out, p.cap_out);
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = fabsf(sv[e]);
+#pragma unroll
+        for (int j = 8; j < 64; j += 8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], fabsf(sv[j + e]));
+        const float big = max3f(max3f(t[0], t[1], t[2]), max3f(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
+        if (__any_sync(0xffffffffu, big * p.cap_in > 1.f)) {
+          // some score of the warp is past the cap
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = tanh_any(sv[j] * p.cap_in) * p.cap_out;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            const float2 y = mul2(tanh_poly2(mul2(make_float2(sv[j], sv[j + 1]), ci)), co);
+            sv[j] = y.x;
+            sv[j + 1] = y.y;
+          }
+        }
+      } else if (bias_on) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) sv[j] *= p.scale_log2;
+      }
+      if (bias_on) {
+        const int n0 = (tr.kv_begin + it) * kTileN + hf * 64;
+        const float base = shared ? (float)(pos_q - n0) : (float)(m_v - n0);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) sv[j] = fmaf(nslope2, fabsf(base - (float)j), sv[j]);
+      }
+    };
+    // zeros over the V rows of tile it outside [z0, z1) (thread r: row r), so
+    // that whatever lies there, NaN included, adds nothing through P = 0
+    auto clear_v_rows = [&](int it, int z0, int z1) -> bool {
+      const int st = it % kStages;
+      if (!mbar_wait(&full_v[st], (uint32_t)(it / kStages) & 1u, p.err, abort_flag)) return false;
+      const int j = (tr.kv_begin + it) * kTileN + r;
+      if (j < z0 || j >= z1) {
+        uint8_t* vt = smem + C::kRing + st * C::kStageBytes + NSTREAM * C::kTile;
+#pragma unroll 1
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4*>(vt + (i / 8) * kChunkBytes + r * 128 + (i % 8) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      return true;
     };
     // -inf outside the row's key set, on edge and global tiles: a keep-mask
     // of the half's 64 keys (bit j: key j is in the set) applied by one
@@ -843,6 +1008,14 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       const bool edge = ((!glob || it < n_band) && !(t_kv >= int_lo && t_kv <= int_hi)) ||
                         (inplace && t_kv * kTileN < gap_hi && t_kv * kTileN + kTileN > gap_lo);
 
+      if (scored) {
+        // padding rows, and pool rows past the prefix, may hold anything
+        const int z0 = docs ? dt.c0 : 0, z1 = docs ? dt.cn : p.N;
+        if (t_kv * kTileN < z0 || t_kv * kTileN + kTileN > z1) {
+          if (!__all_sync(0xffffffffu, clear_v_rows(it, z0, z1))) { ok = false; break; }
+        }
+      }
+
       // adopt a larger max seen on the previous tile (rare after the start)
       const bool pend = m_pend > m_used;
       if (__any_sync(0xffffffffu, pend)) {
@@ -865,6 +1038,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
         zero_p(64 * e);
       } else {
       read_half(e, sv);
+      if (scored) shape_half(it, e, sv);
       mask_half(it, e, edge, sv);
       if (!__any_sync(0xffffffffu, m_used == -INFINITY)) {
         // optimistic: exponentiate against the running max while the half's
@@ -911,6 +1085,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       // these columns now belong to the early half of the next tile
       tc_fence_before();
       mbar_arrive(&l_free[slot]);
+      if (scored) shape_half(it, e ^ 1, sv);
       mask_half(it, e ^ 1, edge, sv);
       if (!__any_sync(0xffffffffu, m_used == -INFINITY)) {
         // optimistic as above; on a jump O must also hold the early half's
@@ -968,12 +1143,19 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 
     // split key walk: this CTA's part goes to the partials (fp32 O / l and
     // lse); an empty part contributes nothing (lse = -inf)
-    const bool split = qwin && p.nsplit > 1 && !pair;
-    const size_t prow = (((size_t)sp * p.B + b) * p.H + h) * (size_t)Mq + m_row;
+    const bool split = shared || (qwin && p.nsplit > 1 && !pair);
+    const size_t prow = shared ? ((size_t)sp * p.B + sR / grp) * p.H + h
+                               : (((size_t)sp * p.B + b) * p.H + h) * (size_t)Mq + m_row;
     if (split && ok && n_tiles == 0 && row_valid && !warp_idle) {
       float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D);
       for (int e = 0; e < D / 4; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       p.part_lse[prow] = -INFINITY;
+    }
+    if (docs && ok && n_tiles == 0 && row_valid) {
+      // a tile of padding rows
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (((size_t)b * p.N + m_row) * p.H + h) * D);
+      for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse) p.lse[((size_t)b * p.H + h) * p.N + m_row] = -INFINITY;
     }
     bool fin = ok && n_tiles > 0 && !warp_idle;
     if (fin) fin = mbar_wait(&o_final[slot], 0, p.err, abort_flag);
@@ -1081,9 +1263,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       }
     } else if (__all_sync(0xffffffffu, fin)) {
       tc_fence_after();
-      // (l == 0: a part of a split walk with none of the row's keys; its
-      // lse is -inf and the merge skips it)
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // (l == 0: a part of a split walk with none of the row's keys, whose
+      // lse is -inf and which the merge skips, or a padding row: zeros)
+      // (the polynomial exponential leaves 2^-125 of a masked score, so l of a
+      // row without keys need not be 0; its maximum tells)
+      const bool none = scored && m_used == -INFINITY;
+      const float inv = l > 0.f && !none ? 1.f / l : 0.f;
       const size_t orow_i = qwin ? (size_t)b * Mq + m_row : (size_t)b * p.N + i_phys;
       uint16_t* orow = p.out + (orow_i * p.H + h) * D;
       // rows start on 128-byte multiples from out: 32-byte stores when out
@@ -1097,6 +1282,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
         tmem_ld32(tO + j2 * 64, v[0]);
         tmem_ld32(tO + j2 * 64 + 32, v[1]);
         tmem_wait_ld();
+        if (none) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[0][e] = v[1][e] = 0u;
+        }
         if (split) {
           if (row_valid) {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + j2 * 64);
@@ -1130,7 +1319,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
           }
         }
       }
-      const float lse_v = (m_used + __log2f(l)) * 0.69314718055994531f;
+      const float lse_v = none ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
       if (row_valid && split)
         p.part_lse[prow] = lse_v;
       else if (row_valid && p.lse)
@@ -1192,16 +1381,29 @@ bool pair_clusters_fit() {
   return k > 0;
 }
 
+void set_score(FwdParams& p, const ScoreArgs& sc, float scale) {
+  if (sc.softcap > 0.f) {
+    p.cap_in = scale / sc.softcap;
+    p.cap_out = sc.softcap * 1.4426950408889634f;
+  }
+  p.slopes = sc.slopes;
+  p.cu_docs = sc.cu_docs;
+  p.doc_pre = sc.prefix;
+  p.n_docs = sc.n_docs;
+}
+
 template <int D, int NSLOT, int NSTREAM>
 int launch_impl(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H,
                 int Hkv, int N, int L, int R, int d, int bs, const int32_t* G, int ng,
-                float scale, cudaStream_t stream, const QueryWindow* qw, int qt_lo, int qt_hi) {
+                float scale, cudaStream_t stream, const QueryWindow* qw, int qt_lo, int qt_hi,
+                const ScoreArgs* sc = nullptr) {
   using C = Cfg<D, NSLOT, NSTREAM>;
-  static std::atomic<unsigned long long> attr_kind[3] = {{0}, {0}, {0}};
-  const int kind = qw ? 1 : (ng > 0 ? 2 : 0);
-  const void* kfn[3] = {reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 0>),
+  static std::atomic<unsigned long long> attr_kind[4] = {{0}, {0}, {0}, {0}};
+  const int kind = sc ? 3 : (qw ? 1 : (ng > 0 ? 2 : 0));
+  const void* kfn[4] = {reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 0>),
                         reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 1>),
-                        reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 2>)};
+                        reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 2>),
+                        reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 3>)};
   if (!smem_attr_once(kfn[kind], C::kAlloc, attr_kind[kind])) return SWA_ERR_CUDA;
   if (NSLOT == 2 || C::kMinBlocks == 2) {
     // The register split (warpgroup 0: 56 per thread, each softmax
@@ -1209,7 +1411,7 @@ int launch_impl(const void* q, const void* k, const void* v, void* out, float* l
     // block is launched with, or setmaxnreg.inc would never return: checked
     // once per kernel form.
     const long need = NSLOT == 2 ? 128L * 56 + 256L * 208 : 128L * 56 + 128L * 200;
-    static std::atomic<int> regs_ok[3] = {{0}, {0}, {0}};
+    static std::atomic<int> regs_ok[4] = {{0}, {0}, {0}, {0}};
     if (regs_ok[kind].load(std::memory_order_acquire) == 0) {
       cudaFuncAttributes fa;
       if (cudaFuncGetAttributes(&fa, kfn[kind]) != cudaSuccess) return SWA_ERR_CUDA;
@@ -1250,6 +1452,7 @@ int launch_impl(const void* q, const void* k, const void* v, void* out, float* l
       const int rows_q = qw ? qw->Mq : p.Mv[cl];
       p.qtile_prefix[cl + 1] = p.qtile_prefix[cl] + (rows_q + kTileM - 1) / kTileM;
     }
+    if (sc) set_score(p, *sc, scale);
     if (qt_hi >= 0) {
       // a row-range launch (one class): only query tiles [qt_lo, qt_hi)
       if (geo.nclass != 1 || qw) return SWA_ERR_UNSUPPORTED;
@@ -1365,6 +1568,9 @@ int launch_impl(const void* q, const void* k, const void* v, void* out, float* l
     } else if (kind == 1)
       swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 1><<<(unsigned)grid, C::kThreads, C::kAlloc,
                                                    stream>>>(p);
+    else if (kind == 3)
+      swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 3><<<(unsigned)grid, C::kThreads, C::kAlloc,
+                                                   stream>>>(p);
     else if (kind == 2)
       swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 2><<<(unsigned)grid, C::kThreads, C::kAlloc,
                                                    stream>>>(p);
@@ -1376,7 +1582,103 @@ int launch_impl(const void* q, const void* k, const void* v, void* out, float* l
   return SWA_OK;
 }
 
+// The register split of the forms that use setmaxnreg (see launch_impl).
+template <int D, int NSLOT>
+bool shared_regs_fit() {
+  using C = Cfg<D, NSLOT, 1>;
+  if (!(NSLOT == 2 || C::kMinBlocks == 2)) return true;
+  const long need = NSLOT == 2 ? 128L * 56 + 256L * 208 : 128L * 56 + 128L * 200;
+  static std::atomic<int> known{0};
+  if (known.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, swa_fwd_sm100_kernel<D, NSLOT, 1, 4>) != cudaSuccess)
+      return false;
+    known.store((long)fa.numRegs * C::kThreads >= need ? 1 : -1, std::memory_order_release);
+  }
+  return known.load(std::memory_order_acquire) > 0;
+}
+
+template <int D, int NSLOT>
+int launch_prefix_impl(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
+                       cudaStream_t stream) {
+  using C = Cfg<D, NSLOT, 1>;
+  static std::atomic<unsigned long long> attr{0};
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, 1, 4>),
+                      C::kAlloc, attr))
+    return SWA_ERR_CUDA;
+  if (!shared_regs_fit<D, NSLOT>()) return SWA_ERR_UNSUPPORTED;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.err = device_error_word();
+  if (!p.err) return SWA_ERR_CUDA;
+  p.q_raw = static_cast<const uint16_t*>(a.q);
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.N = a.n_prefix;
+  p.L = -1;
+  p.R = -1;
+  p.d = 1;
+  p.nclass = 1;
+  p.Mv[0] = a.n_prefix;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  ScoreArgs sc;
+  sc.softcap = a.softcap;
+  sc.slopes = a.slopes;
+  set_score(p, sc, a.scale);
+  p.pos0 = a.pos;
+  p.win = a.W;
+  p.keep = a.keep;
+  p.table = a.prefix_table;
+  p.page_size = a.page_size;
+  p.num_pages = a.num_pages;
+  p.nsplit = nsplit;
+  p.part_o = part_o;
+  p.part_lse = part_lse;
+  const int pool_rows = a.num_pages * a.page_size;
+  if (encode_kv_map(&p.tmK[0], a.k_pages, D, a.Hkv, pool_rows, 1) != SWA_OK ||
+      encode_kv_map(&p.tmV[0], a.v_pages, D, a.Hkv, pool_rows, 1) != SWA_OK)
+    return SWA_ERR_CUDA;
+  const long long rows = (long long)a.B * (a.H / a.Hkv);
+  const long long grid = (rows + NSLOT * kTileM - 1) / (NSLOT * kTileM) * a.Hkv * nsplit;
+  if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
+  swa_fwd_sm100_kernel<D, NSLOT, 1, 4><<<(unsigned)grid, C::kThreads, C::kAlloc, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
 }  // namespace
+
+int launch_fwd_scored(const void* q, const void* k, const void* v, void* out, float* lse, int B,
+                      int H, int Hkv, int N, int D, int L, int R, const ScoreArgs& sc, float scale,
+                      cudaStream_t stream) {
+  if (sc.plain())
+    return launch_fwd_sm100(q, k, v, out, lse, B, H, Hkv, N, D, L, R, 1, 0, nullptr, 0, scale,
+                            stream);
+  const bool gqa_pair = (H / Hkv) % 2 == 0;
+  if (D == 128)
+    return gqa_pair ? launch_impl<128, 2, 1>(q, k, v, out, lse, B, H, Hkv, N, L, R, 1, 0, nullptr,
+                                             0, scale, stream, nullptr, 0, -1, &sc)
+                    : launch_impl<128, 1, 1>(q, k, v, out, lse, B, H, Hkv, N, L, R, 1, 0, nullptr,
+                                             0, scale, stream, nullptr, 0, -1, &sc);
+  if (D == 64)
+    return gqa_pair ? launch_impl<64, 2, 1>(q, k, v, out, lse, B, H, Hkv, N, L, R, 1, 0, nullptr,
+                                            0, scale, stream, nullptr, 0, -1, &sc)
+                    : launch_impl<64, 1, 1>(q, k, v, out, lse, B, H, Hkv, N, L, R, 1, 0, nullptr,
+                                            0, scale, stream, nullptr, 0, -1, &sc);
+  return SWA_ERR_UNSUPPORTED;
+}
+
+int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
+                  cudaStream_t stream) {
+  const bool two = (long long)a.B * (a.H / a.Hkv) > kTileM;  // more than one query tile
+  if (a.D == 128)
+    return two ? launch_prefix_impl<128, 2>(a, nsplit, part_o, part_lse, stream)
+               : launch_prefix_impl<128, 1>(a, nsplit, part_o, part_lse, stream);
+  if (a.D == 64)
+    return two ? launch_prefix_impl<64, 2>(a, nsplit, part_o, part_lse, stream)
+               : launch_prefix_impl<64, 1>(a, nsplit, part_o, part_lse, stream);
+  return SWA_ERR_UNSUPPORTED;
+}
 
 bool fwd_qwin_stacks(int H, int Hkv, int Mq) {
   const int grp = H / Hkv;

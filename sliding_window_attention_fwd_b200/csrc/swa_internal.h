@@ -87,6 +87,62 @@ int launch_fwd_sm100(const void* q, const void* k, const void* v, void* out, flo
                      const int32_t* G, int ng, float scale, cudaStream_t stream,
                      const QueryWindow* qw = nullptr, int qt_lo = 0, int qt_hi = -1);
 
+// Shaped scores (swa_score.cuh): every field as in swa_score of swa.h.
+struct ScoreArgs {
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  const int32_t* cu_docs = nullptr;
+  const int32_t* prefix = nullptr;
+  int n_docs = 0;
+  // nothing shaped: the band kernels' case
+  bool plain() const { return !(softcap > 0.f) && !slopes && !cu_docs; }
+};
+int launch_fwd_scored(const void* q, const void* k, const void* v, void* out, float* lse, int B,
+                      int H, int Hkv, int N, int D, int L, int R, const ScoreArgs& sc, float scale,
+                      cudaStream_t stream);
+// Its gradients; delta: [B, H, N] fp32 workspace.
+int launch_bwd_scored(const void* q, const void* k, const void* v, const void* out,
+                      const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                      float* delta, int B, int H, int Hkv, int N, int D, int L, int R,
+                      const ScoreArgs& sc, float scale, cudaStream_t stream);
+
+// Decode of a batch whose sequences begin with the same n_prefix tokens.
+struct SharedArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  void* out;
+  float* lse;
+  const int32_t* prefix_table;
+  const int32_t* table;
+  const int64_t* pos;
+  int B, H, Hkv, D, page_size, num_pages, max_pages, n_prefix, W, keep, max_tail;
+  float scale, softcap;
+  const float* slopes;
+};
+// How the keys of a call are split: parts of the prefix and of the own keys
+// (part_keys keys each, the last part taking what is left).
+struct SharedPlan {
+  int prefix_parts, own_parts, part_keys;
+  size_t bytes;  // workspace: O / l and lse of every part
+};
+SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int max_tail);
+int launch_decode_shared(const SharedArgs& a, const SharedPlan& pl, void* workspace,
+                         cudaStream_t stream);
+// The prefix's share: parts 0 .. nsplit - 1 of the partial results.
+int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
+                  cudaStream_t stream);
+// The own keys' share (swa_decode_tc.cu).
+int launch_own(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
+               cudaStream_t stream);
+
+int launch_rope_append(const void* q, const void* k, const void* v, long long q_stride,
+                       long long k_stride, long long v_stride, const float* inv_freq, int rot,
+                       int interleaved, const int32_t* cu, const int64_t* pos0,
+                       const int32_t* table, void* q_out, long long qo_stride, void* k_pages,
+                       void* v_pages, int T, int B, int H, int Hkv, int D, int page_size,
+                       int num_pages, int max_pages, cudaStream_t stream);
+
 int launch_decode(const void* q, const void* k_ring, const void* v_ring, void* out,
                   float* lse, const int64_t* pos, int B, int H, int Hkv, int D, int W,
                   float scale, cudaStream_t stream);
