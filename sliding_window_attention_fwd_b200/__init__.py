@@ -51,7 +51,8 @@ def __getattr__(name):
     if name in _EXPORTS:
         from . import binding
 
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # later uses skip this function
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

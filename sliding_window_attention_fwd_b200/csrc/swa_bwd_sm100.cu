@@ -38,6 +38,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "swa_internal.h"
 #include "swa_ptx.cuh"
@@ -94,7 +95,7 @@ struct BwdTcParams {
   int Mv[kMaxClassesB];
   float scale, scale_log2;
   // shaped scores (swa_score.cuh), fields as in the forward
-  float cap_in, cap_out;
+  CapCoefs cap;
   const float* slopes;
   const int32_t* cu_docs;
   const int32_t* doc_pre;
@@ -150,37 +151,58 @@ __device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
   return make_float2(ex2_approx(x.x), ex2_approx(x.y));
 }
 
-// Shaped scores of 32 raw products: x = cap(scale qk) - slope |i - j| - lse,
-// all in log2 units, and fac = 1 - tanh^2, the cap's derivative (1 without a
-// cap).  d0 + dj: signed distance of the first of the 32 and its step (+-1).
+// Shaped scores of 32 raw products of one thread (its row r against the
+// columns c0 .. c0 + 31): x = cap(scale qk) - slope |i - j| in log2 units, and
+// fac = 1 - tanh^2, the cap's derivative.  The bias is linear in the column
+// while the chunk lies on one side of every row of the warp (add0, step: of
+// the columns 2e, 2e + 1); on the diagonal it takes |i - j| per column.
+template <int SC>
 struct Shape {
-  float cap_in, cap_out, scale_log2, nslope2;  // nslope2 0: no bias
-  // u values of the chunk -> whether all lie in the polynomial's range, for
-  // the whole warp
-  __device__ __forceinline__ bool small(const uint32_t (&sv)[32]) const {
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 add0, step;
+  float base, nslope2;
+  bool diag, small;
+  __device__ __forceinline__ Shape(const CapCoefs& c, float nslope2_, const uint32_t (&sv)[32],
+                                   int r, int c0) {
+    add0 = step = make_float2(0.f, 0.f);
+    base = 0.f;
+    diag = false;
+    small = true;
+    nslope2 = nslope2_;
+    if (SC & 2) {
+      const int lo = r - (int)(threadIdx.x & 31) - c0;  // the warp's first row
+      base = (float)(r - c0);
+      diag = lo < 31 && lo + 31 > 0;
+      const float k1 = lo >= 31 ? -nslope2 : nslope2;
+      add0 = make_float2(-k1 * base, fmaf(-k1, base, k1));
+      step = make_float2(2.f * k1, 2.f * k1);
+    }
+    if (SC & 1) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], fabsf(__uint_as_float(sv[e])));
-    const float m = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-    return !__any_sync(0xffffffffu, m * cap_in > 1.f);
+      for (int e = 0; e < 32; e += 2)
+        t[e / 2 & 3] = max3f(t[e / 2 & 3], fabsf(__uint_as_float(sv[e])),
+                             fabsf(__uint_as_float(sv[e + 1])));
+      small = !__any_sync(0xffffffffu, max3f(t[0], t[1], fmaxf(t[2], t[3])) > c.small);
+    }
   }
-  __device__ __forceinline__ float2 pair(float a, float b, bool poly, float dist0, float dist1,
-                                         float2 nlse, float2* fac) const {
-    float2 x;
-    if (cap_in > 0.f) {
-      const float2 u = mul2(make_float2(a, b), make_float2(cap_in, cap_in));
-      const float2 t = poly ? tanh_poly2(u) : make_float2(tanh_any(u.x), tanh_any(u.y));
-      x = fma2(t, make_float2(cap_out, cap_out), nlse);
-      *fac = fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
-    } else {
-      x = fma2(make_float2(a, b), make_float2(scale_log2, scale_log2), nlse);
-      *fac = make_float2(1.f, 1.f);
+  // Columns 2e and 2e + 1, nl being -lse.
+  template <bool kSmall>
+  __device__ __forceinline__ float2 pair(const CapCoefs& c, float scale_log2, float2 s, int e,
+                                         float2 nl, float2* fac) const {
+    if (SC & 2) {
+      if (diag)
+        nl = make_float2(fmaf(nslope2, fabsf(base - (float)(2 * e)), nl.x),
+                         fmaf(nslope2, fabsf(base - (float)(2 * e + 1)), nl.y));
+      else
+        nl = add2(nl, fma2(make_float2((float)e, (float)e), step, add0));
     }
-    if (nslope2 != 0.f) {
-      x.x = fmaf(nslope2, fabsf(dist0), x.x);
-      x.y = fmaf(nslope2, fabsf(dist1), x.y);
+    if (SC & 1) {
+      const float2 t =
+          kSmall ? tanh_small(c, s) : make_float2(tanh_any(c, s.x), tanh_any(c, s.y));
+      *fac = fma2(mul2(t, t), make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+      return fma2(t, make_float2(c.out, c.out), nl);
     }
-    return x;
+    return fma2(s, make_float2(scale_log2, scale_log2), nl);
   }
 };
 
@@ -197,8 +219,9 @@ __device__ __forceinline__ void clear_row(uint8_t* tile, int r, int row0, int z0
 }
 
 // ======================================================== dq kernel
-// kShaped: shaped scores and documents (token-level band, no dilation).
-template <int D, bool kShaped>
+// kShaped: shaped scores and documents (token-level band, no dilation); SC: 1
+// a cap, 2 a bias, 3 both.
+template <int D, bool kShaped, int SC>
 __global__ void __launch_bounds__(kThreadsB, 1)
     swa_bwd_dq_kernel(const __grid_constant__ BwdTcParams p) {
   using C = BCfg<D>;
@@ -382,15 +405,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     interior_tiles(geo, Mv, qt, &int_lo, &int_hi);
     const float sl2 = p.scale_log2;
     bool real_row = row_valid;  // a row of some document
-    Shape shp{p.cap_in, p.cap_out, p.scale_log2, 0.f};
+    float nslope2 = 0.f;
     if (kShaped) {
-      const DocSpan ds = dm.of_thread(m_v, dt.mlo, dt.mhi);
+      const DocSpan ds = dm.of_thread(dt, m_v);
       real_row = row_valid && ds.start < ds.end;
       klo = real_row ? dm.key_first(ds, m_v) : 1;
       khi = real_row ? dm.key_last(ds, m_v) : 0;
       int_lo = dt.int_lo;
       int_hi = dt.int_hi;
-      if (p.slopes) shp.nslope2 = -__ldg(p.slopes + h) * kLog2e;
+      if (SC & 2) nslope2 = -__ldg(p.slopes + h) * kLog2e;
     }
     // Delta_i = dO_i . out_i (each group sums a quarter of the row, the
     // parts meet in shared memory) and lse in log2 units; rows past the
@@ -447,29 +470,45 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld32(tS + 32 * ch, sv);
         tmem_wait_ld();
         const int n0 = t * kTileN + 32 * ch;
-        const bool poly = kShaped && p.cap_in > 0.f && shp.small(sv);
-        const float d0 = kShaped ? (float)(m_v - n0) : 0.f;  // distance to the chunk's first key
+        if constexpr (kShaped) {
+          const Shape<SC> shp(p.cap, nslope2, sv, m_v, n0);
+          auto columns = [&](auto is_small) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 xs, fac;
-          if (kShaped)
-            xs = shp.pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]), poly,
-                          d0 - (float)(2 * e), d0 - (float)(2 * e + 1),
-                          make_float2(-lse2, -lse2), &fac);
-          else
-            xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
-                      make_float2(sl2, sl2), make_float2(-lse2, -lse2));
-          if (edge) {
-            const int j0 = n0 + 2 * e;
-            if (!(j0 >= klo && j0 <= khi && j0 < Mv)) xs.x = -INFINITY;
-            if (!(j0 + 1 >= klo && j0 + 1 <= khi && j0 + 1 < Mv)) xs.y = -INFINITY;
-          }
-          pr[i][e] = exp2_pair(xs, (e & 1) != 0 && !edge);
-          if (kShaped && p.cap_in > 0.f) {
-            // a masked score may be NaN: its factor must not meet P = 0
-            const float2 f = mul2(pr[i][e], fac);
-            pr[i][e] = make_float2(edge && pr[i][e].x == 0.f ? 0.f : f.x,
-                                   edge && pr[i][e].y == 0.f ? 0.f : f.y);
+            for (int e = 0; e < 16; ++e) {
+              float2 fac;
+              float2 xs = shp.template pair<decltype(is_small)::value>(
+                  p.cap, sl2, make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
+                  e, make_float2(-lse2, -lse2), &fac);
+              if (edge) {
+                const int j0 = n0 + 2 * e;
+                if (!(j0 >= klo && j0 <= khi)) xs.x = -INFINITY;
+                if (!(j0 + 1 >= klo && j0 + 1 <= khi)) xs.y = -INFINITY;
+              }
+              // (with a cap the FMA pipe has enough to do)
+              pr[i][e] = exp2_pair(xs, !(SC & 1) && (e & 1) != 0 && !edge);
+              if (SC & 1) {
+                if (edge) {  // a masked product may be NaN: its factor must not meet P = 0
+                  if (xs.x == -INFINITY) fac.x = 0.f;
+                  if (xs.y == -INFINITY) fac.y = 0.f;
+                }
+                pr[i][e] = mul2(pr[i][e], fac);
+              }
+            }
+          };
+          if (shp.small) columns(std::true_type());
+          else columns(std::false_type());
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 xs =
+                fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
+                     make_float2(sl2, sl2), make_float2(-lse2, -lse2));
+            if (edge) {
+              const int j0 = n0 + 2 * e;
+              if (!(j0 >= klo && j0 <= khi && j0 < Mv)) xs.x = -INFINITY;
+              if (!(j0 + 1 >= klo && j0 + 1 <= khi && j0 + 1 < Mv)) xs.y = -INFINITY;
+            }
+            pr[i][e] = exp2_pair(xs, (e & 1) != 0 && !edge);
           }
         }
       }
@@ -497,14 +536,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         uint32_t dpv[32];
         tmem_ld32(tP + 32 * ch, dpv);
         tmem_wait_ld();
+        if (kShaped && edge) {
+          // dP of masked places may be NaN (padding): 0 there
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (pr[i][e].x == 0.f) dpv[2 * e] = 0u;
+            if (pr[i][e].y == 0.f) dpv[2 * e + 1] = 0u;
+          }
+        }
         const float2 ndl = make_float2(-delta, -delta);
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
-                                                      __uint_as_float(dpv[2 * e + 1])), ndl));
-          if (kShaped && edge)
-            ds = make_float2(pr[i][e].x == 0.f ? 0.f : ds.x, pr[i][e].y == 0.f ? 0.f : ds.y);
+          const float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
+                                                            __uint_as_float(dpv[2 * e + 1])), ndl));
           pk[e] = pack_bf16x2(ds.x, ds.y);
         }
         // dS of these 32 keys over the group's own (already read) S columns
@@ -559,7 +604,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 }
 
 // ======================================================== dk / dv kernel
-template <int D, bool kShaped>
+template <int D, bool kShaped, int SC>
 __global__ void __launch_bounds__(kThreadsB, 1)
     swa_bwd_dkdv_kernel(const __grid_constant__ BwdTcParams p) {
   using C = BCfg<D>;
@@ -767,9 +812,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     int int_lo, int_hi;
     interior_qtiles_keys(geo, Mv, kt * kTileN, &int_lo, &int_hi);
     const float sl2 = p.scale_log2;
-    Shape shp{p.cap_in, p.cap_out, p.scale_log2, 0.f};
     if (kShaped) {
-      const DocSpan ds = dm.of_thread(j_v, dt.mlo, dt.mhi);
+      const DocSpan ds = dm.of_thread(dt, j_v);
       const bool real_key = key_valid && ds.start < ds.end;
       qlo = real_key ? dm.query_first(ds, j_v) : 1;
       qhi = real_key ? dm.query_last(ds, j_v) : 0;
@@ -780,8 +824,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     for (int s = 0; s < n_steps; ++s) {
       const int st = s % S_;
       const int qt = qr.kv_begin + s / grp;
-      if (kShaped && p.slopes)
-        shp.nslope2 = -__ldg(p.slopes + g_kv * grp + s % grp) * kLog2e;
+      const float nslope2 =
+          (SC & 2) ? -__ldg(p.slopes + g_kv * grp + s % grp) * kLog2e : 0.f;
       const bool edge = !(qt >= int_lo && qt <= int_hi);
       // P^T as soon as S^T is in TMEM (dP^T is still being computed)
       bool w = mbar_wait(st_full, (uint32_t)s & 1u, p.err, abort_flag);
@@ -799,35 +843,57 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld32(tS + 32 * ch, sv);
         tmem_wait_ld();
         const int i0 = qt * kTileM + 32 * ch;
-        const bool poly = kShaped && p.cap_in > 0.f && shp.small(sv);
-        const float d0 = kShaped ? (float)(i0 - j_v) : 0.f;  // distance of the chunk's first row
         const float4* l4 = reinterpret_cast<const float4*>(vl + 32 * ch);
         uint32_t pp[16];
+        if constexpr (kShaped) {
+          const Shape<SC> shp(p.cap, nslope2, sv, j_v, i0);
+          auto columns = [&](auto is_small) {
 #pragma unroll
-        for (int e2 = 0; e2 < 8; ++e2) {
-          const float4 l = l4[e2];  // lse2 of this pair of pairs
+            for (int e2 = 0; e2 < 8; ++e2) {
+              const float4 l = l4[e2];  // lse2 of this pair of pairs
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            const int e = 2 * e2 + h2;
-            const float2 lp = h2 ? make_float2(l.z, l.w) : make_float2(l.x, l.y);
-            float2 xs, fac;
-            if (kShaped)
-              xs = shp.pair(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]), poly,
-                            d0 + (float)(2 * e), d0 + (float)(2 * e + 1),
-                            make_float2(-lp.x, -lp.y), &fac);
-            else
-              xs = fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
-                        make_float2(sl2, sl2), make_float2(-lp.x, -lp.y));
-            if (edge) {
-              if (!(i0 + 2 * e >= qlo && i0 + 2 * e <= qhi)) xs.x = -INFINITY;
-              if (!(i0 + 2 * e + 1 >= qlo && i0 + 2 * e + 1 <= qhi)) xs.y = -INFINITY;
+              for (int h2 = 0; h2 < 2; ++h2) {
+                const int e = 2 * e2 + h2;
+                float2 fac;
+                float2 xs = shp.template pair<decltype(is_small)::value>(
+                    p.cap, sl2,
+                    make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), e,
+                    h2 ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y), &fac);
+                if (edge) {
+                  if (!(i0 + 2 * e >= qlo && i0 + 2 * e <= qhi)) xs.x = -INFINITY;
+                  if (!(i0 + 2 * e + 1 >= qlo && i0 + 2 * e + 1 <= qhi)) xs.y = -INFINITY;
+                }
+                pr[i][e] = exp2_pair(xs, !(SC & 1) && h2 != 0 && !edge);
+                pp[e] = pack_bf16x2(pr[i][e].x, pr[i][e].y);
+                if (SC & 1) {
+                  if (edge) {
+                    if (xs.x == -INFINITY) fac.x = 0.f;
+                    if (xs.y == -INFINITY) fac.y = 0.f;
+                  }
+                  pr[i][e] = mul2(pr[i][e], fac);
+                }
+              }
             }
-            pr[i][e] = exp2_pair(xs, h2 != 0 && !edge);
-            pp[e] = pack_bf16x2(pr[i][e].x, pr[i][e].y);
-            if (kShaped && p.cap_in > 0.f) {
-              const float2 f = mul2(pr[i][e], fac);
-              pr[i][e] = make_float2(edge && pr[i][e].x == 0.f ? 0.f : f.x,
-                                     edge && pr[i][e].y == 0.f ? 0.f : f.y);
+          };
+          if (shp.small) columns(std::true_type());
+          else columns(std::false_type());
+        } else {
+#pragma unroll
+          for (int e2 = 0; e2 < 8; ++e2) {
+            const float4 l = l4[e2];  // lse2 of this pair of pairs
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const int e = 2 * e2 + h2;
+              const float2 lp = h2 ? make_float2(l.z, l.w) : make_float2(l.x, l.y);
+              float2 xs =
+                  fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
+                       make_float2(sl2, sl2), make_float2(-lp.x, -lp.y));
+              if (edge) {
+                if (!(i0 + 2 * e >= qlo && i0 + 2 * e <= qhi)) xs.x = -INFINITY;
+                if (!(i0 + 2 * e + 1 >= qlo && i0 + 2 * e + 1 <= qhi)) xs.y = -INFINITY;
+              }
+              pr[i][e] = exp2_pair(xs, h2 != 0 && !edge);
+              pp[e] = pack_bf16x2(pr[i][e].x, pr[i][e].y);
             }
           }
         }
@@ -867,6 +933,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         uint32_t dpv[32];
         tmem_ld32(tP + 32 * ch, dpv);
         tmem_wait_ld();
+        if (kShaped && edge) {
+          // dP of masked places may be NaN (padding): 0 there
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (pr[i][e].x == 0.f) dpv[2 * e] = 0u;
+            if (pr[i][e].y == 0.f) dpv[2 * e + 1] = 0u;
+          }
+        }
         const float4* d4 = reinterpret_cast<const float4*>(vl + kTileM + 32 * ch);
         uint32_t pd[16];
 #pragma unroll
@@ -876,10 +950,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int h2 = 0; h2 < 2; ++h2) {
             const int e = 2 * e2 + h2;
             const float2 dn = h2 ? make_float2(-dl.z, -dl.w) : make_float2(-dl.x, -dl.y);
-            float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
-                                                        __uint_as_float(dpv[2 * e + 1])), dn));
-            if (kShaped && edge)
-              ds = make_float2(pr[i][e].x == 0.f ? 0.f : ds.x, pr[i][e].y == 0.f ? 0.f : ds.y);
+            const float2 ds = mul2(pr[i][e], add2(make_float2(__uint_as_float(dpv[2 * e]),
+                                                              __uint_as_float(dpv[2 * e + 1])), dn));
             pd[e] = pack_bf16x2(ds.x, ds.y);
           }
         }
@@ -936,15 +1008,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
 }
 
-template <int D, bool kShaped>
+template <int D, bool kShaped, int SC>
 int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* out,
                        const void* dout, const float* lse, void* dq, void* dk, void* dv,
                        float* delta, int B, int H, int Hkv, int N, int L, int R, int d, int bs,
                        float scale, cudaStream_t stream, const ScoreArgs* sc = nullptr) {
   using C = BCfg<D>;
   static std::atomic<unsigned long long> attr_dq{0}, attr_dkdv{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D, kShaped>), C::kAlloc, attr_dq) ||
-      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D, kShaped>), C::kAlloc,
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D, kShaped, SC>), C::kAlloc, attr_dq) ||
+      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D, kShaped, SC>), C::kAlloc,
                       attr_dkdv))
     return SWA_ERR_CUDA;
   int* err = device_error_word();
@@ -979,10 +1051,7 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
       p.scale = scale;
       p.scale_log2 = scale * kLog2e;
       if (kShaped) {
-        if (sc->softcap > 0.f) {
-          p.cap_in = scale / sc->softcap;
-          p.cap_out = sc->softcap * kLog2e;
-        }
+        p.cap = cap_coefs(sc->softcap, scale, false);
         p.slopes = sc->slopes;
         p.cu_docs = sc->cu_docs;
         p.doc_pre = sc->prefix;
@@ -1025,12 +1094,12 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
         const long grid = ntiles * B * H;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
-        swa_bwd_dq_kernel<D, kShaped><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
+        swa_bwd_dq_kernel<D, kShaped, SC><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
       } else {
         const long grid = ntiles * B * Hkv;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
-        swa_bwd_dkdv_kernel<D, kShaped><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
+        swa_bwd_dkdv_kernel<D, kShaped, SC><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
       }
       if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
     }
@@ -1045,10 +1114,10 @@ int launch_backward_tc(const void* q, const void* k, const void* v, const void* 
                        float* delta, int B, int H, int Hkv, int N, int D, int L, int R, int d,
                        int bs, float scale, cudaStream_t stream) {
   if (D == 128)
-    return launch_bwd_tc_impl<128, false>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L,
+    return launch_bwd_tc_impl<128, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L,
                                    R, d, bs, scale, stream);
   if (D == 64)
-    return launch_bwd_tc_impl<64, false>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, R,
+    return launch_bwd_tc_impl<64, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, R,
                                   d, bs, scale, stream);
   return SWA_ERR_UNSUPPORTED;
 }
@@ -1060,12 +1129,21 @@ int launch_bwd_scored(const void* q, const void* k, const void* v, const void* o
   if (sc.plain())
     return launch_backward_tc(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, D, L, R,
                               1, 0, scale, stream);
-  if (D == 128)
-    return launch_bwd_tc_impl<128, true>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N,
-                                         L, R, 1, 0, scale, stream, &sc);
-  if (D == 64)
-    return launch_bwd_tc_impl<64, true>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N,
-                                        L, R, 1, 0, scale, stream, &sc);
+  auto go = [&](auto d) -> int {
+    constexpr int kD = decltype(d)::value;
+    switch (sc.kind()) {
+#define SWA_BWD_KIND(SC)                                                                        \
+  launch_bwd_tc_impl<kD, true, SC>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, \
+                                   R, 1, 0, scale, stream, &sc)
+      case 0: return SWA_BWD_KIND(0);
+      case 1: return SWA_BWD_KIND(1);
+      case 2: return SWA_BWD_KIND(2);
+      default: return SWA_BWD_KIND(3);
+#undef SWA_BWD_KIND
+    }
+  };
+  if (D == 128) return go(std::integral_constant<int, 128>());
+  if (D == 64) return go(std::integral_constant<int, 64>());
   return SWA_ERR_UNSUPPORTED;
 }
 

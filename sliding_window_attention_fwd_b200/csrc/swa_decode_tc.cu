@@ -63,11 +63,10 @@ struct DecParams {
   int part_keys;  // key indices per CTA (a multiple of 128)
   float scale_log2;
   // behind a shared prefix: only positions >= n_prefix, the last part takes
-  // every key left, a negative position is an inactive sequence; cap_in =
-  // scale / cap and cap_out = cap * log2 e (cap_in 0: no cap), slopes [H] of
-  // the distance bias (NULL: none)
+  // every key left, a negative position is an inactive sequence; the cap, and
+  // slopes [H] of the distance bias (NULL: none)
   int n_prefix, num_pages;
-  float cap_in, cap_out;
+  CapCoefs cap;
   const float* slopes;
 };
 
@@ -360,12 +359,12 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
       const int idx = s0 + t * kTK + r;
       const bool valid = idx < s1 && idx >= lo_idx;
       float xs[kNQ];
-      if (kOwn && (p.cap_in > 0.f || p.slopes)) {
+      if (kOwn && (p.cap.out > 0.f || p.slopes)) {
         const float dist = (float)(pb - a64 - idx);
 #pragma unroll
         for (int n = 0; n < kNQ; ++n) {
           float x = __uint_as_float(sv[n]);
-          x = p.cap_in > 0.f ? tanh_any(x * p.cap_in) * p.cap_out : x * sl2;
+          x = p.cap.out > 0.f ? tanh_any(p.cap, x) * p.cap.out : x * sl2;
           xs[n] = valid ? fmaf(nslope2[n], dist, x) : -INFINITY;
         }
       } else {
@@ -590,10 +589,7 @@ int launch_own_impl(const SharedArgs& a, const SharedPlan& pl, float* part_o, fl
   p.part_keys = pl.part_keys;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.n_prefix = a.n_prefix;
-  if (a.softcap > 0.f) {
-    p.cap_in = a.scale / a.softcap;
-    p.cap_out = a.softcap * 1.4426950408889634f;
-  }
+  p.cap = cap_coefs(a.softcap, a.scale);
   p.slopes = a.slopes;
   const long long grid = (long long)a.B * a.Hkv * pl.own_parts;
   if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;

@@ -95,7 +95,9 @@ struct ScoreArgs {
   const int32_t* prefix = nullptr;
   int n_docs = 0;
   // nothing shaped: the band kernels' case
-  bool plain() const { return !(softcap > 0.f) && !slopes && !cu_docs; }
+  bool plain() const { return kind() == 0 && !cu_docs; }
+  // bit 0: a cap, bit 1: a bias
+  int kind() const { return (softcap > 0.f ? 1 : 0) | (slopes ? 2 : 0); }
 };
 int launch_fwd_scored(const void* q, const void* k, const void* v, void* out, float* lse, int B,
                       int H, int Hkv, int N, int D, int L, int R, const ScoreArgs& sc, float scale,

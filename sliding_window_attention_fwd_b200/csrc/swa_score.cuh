@@ -19,34 +19,64 @@
 
 namespace swa {
 
-// tanh(u) for a pair with |u| <= 1, on the FMA pipe: u times a degree-5
-// polynomial in u^2, fitted to tanh(x)/x on [0, 1] by iterated weighted
-// least squares (relative error 7e-7 evaluated in fp32).  A tanh from MUFU
-// (error 2^-11) would be worth 2 % of a probability at a cap of 50, and the
-// exact form below costs two MUFU operations an element, on the unit that the
-// exponentials already fill.
-__device__ __forceinline__ float2 tanh_poly2(float2 u) {
-  constexpr float kT0 = 0.9999994039535522f, kT1 = -0.3332904279232025f,
-                  kT2 = 0.13281433284282684f, kT3 = -0.051605675369501114f,
-                  kT4 = 0.016743116080760956f, kT5 = -0.003067060373723507f;
-  const float2 z = mul2(u, u);
-  float2 q = fma2(make_float2(kT5, kT5), z, make_float2(kT4, kT4));
-  q = fma2(q, z, make_float2(kT3, kT3));
-  q = fma2(q, z, make_float2(kT2, kT2));
-  q = fma2(q, z, make_float2(kT1, kT1));
-  q = fma2(q, z, make_float2(kT0, kT0));
-  return mul2(u, q);
+// The cap in log2 units as a function of the raw product s: cap log2(e)
+// tanh(s ci) with ci = scale / cap.
+//
+// For |s ci| <= 1/2 (nearly always, with the caps that models use) it is s
+// times a cubic in s^2: a degree-3 polynomial in z fitted to tanh(sqrt z) /
+// sqrt z on [0, 1/4] by iterated weighted least squares (relative error
+// 5.5e-7), its coefficients scaled on the host: four operations on the FMA
+// pipe, none on MUFU, which the exponentials already fill.  A tanh from MUFU
+// (error 2^-11) would be worth 2 % of a probability at a cap of 50.
+// Elsewhere tanh u = 1 - 2 / (e^{2u} + 1) for either sign (absolute error
+// about 2e-7, which is what the score of a cap keeps; +-1 for infinite u,
+// NaN for NaN), with two MUFU operations.
+struct CapCoefs {
+  float a0, a1, a2, a3;  // of s^0 .. s^6, in log2 units (the backward's: of tanh itself)
+  float small;           // the cubic's range of |s|
+  float two_ci_log2e;    // 2 ci log2 e
+  float out;             // cap log2 e (0: no cap)
+};
+
+inline CapCoefs cap_coefs(float softcap, float scale, bool log2_units = true) {
+  CapCoefs c{};
+  if (!(softcap > 0.f)) return c;
+  const double ci = (double)scale / softcap, co = softcap * 1.4426950408889634;
+  const double z = ci * ci, unit = log2_units ? co : 1.0;
+  c.a0 = (float)(0.99999945577 * ci * unit);
+  c.a1 = (float)(-0.33326318 * z * ci * unit);
+  c.a2 = (float)(0.13190297 * z * z * ci * unit);
+  c.a3 = (float)(-0.04440222 * z * z * z * ci * unit);
+  // (outside this range of ci the scaled coefficients would lose bits)
+  c.small = ci > 1e-5 && ci < 1e4 ? (float)(0.5 / ci) : -1.f;
+  c.two_ci_log2e = (float)(2.0 * ci * 1.4426950408889634);
+  c.out = (float)co;
+  return c;
 }
 
-// tanh(u) for any u: the polynomial, or past |u| = 1 the identity tanh |u| =
-// 1 - 2 / (e^{2|u|} + 1) (absolute error about 2e-7 there; +-1 for infinite
-// u, NaN for NaN).
-__device__ __forceinline__ float tanh_any(float u) {
-  if (fabsf(u) > 1.f) {
-    const float e = ex2_approx(fabsf(u) * 2.8853900817779268f);
-    return copysignf(1.f - __fdividef(2.f, e + 1.f), u);
-  }
-  return tanh_poly2(make_float2(u, u)).x;
+// Capped scores of a pair of products plus add.
+__device__ __forceinline__ float2 cap_small(const CapCoefs& c, float2 s, float2 add) {
+  const float2 w = mul2(s, s);
+  float2 q = fma2(make_float2(c.a3, c.a3), w, make_float2(c.a2, c.a2));
+  q = fma2(q, w, make_float2(c.a1, c.a1));
+  q = fma2(q, w, make_float2(c.a0, c.a0));
+  return fma2(s, q, add);
+}
+__device__ __forceinline__ float tanh_any(const CapCoefs& c, float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_approx(s * c.two_ci_log2e) + 1.f));
+  return fmaf(-2.f, r, 1.f);
+}
+// tanh of a pair (coefficients of tanh itself).
+__device__ __forceinline__ float2 tanh_small(const CapCoefs& c, float2 s) {
+  const float2 w = mul2(s, s);
+  float2 q = fma2(make_float2(c.a3, c.a3), w, make_float2(c.a2, c.a2));
+  q = fma2(q, w, make_float2(c.a1, c.a1));
+  q = fma2(q, w, make_float2(c.a0, c.a0));
+  return mul2(s, q);
+}
+__device__ __forceinline__ float2 cap_any(const CapCoefs& c, float2 s, float2 add) {
+  return fma2(make_float2(tanh_any(c, s.x), tanh_any(c, s.y)), make_float2(c.out, c.out), add);
 }
 
 // The documents of one row of tokens.
@@ -54,6 +84,8 @@ struct DocSpan {
   int start, end;  // positions [start, end); start >= end: none (padding)
   int pre;         // end of the prefix (<= start: none)
 };
+
+struct DocTiles;
 
 struct DocMask {
   const int32_t* cu;   // [n + 1] boundaries (NULL: one document [0, N))
@@ -95,27 +127,7 @@ struct DocMask {
     }
     return lo - 1;
   }
-  // The document of row i, for a whole warp at once.
-  __device__ __forceinline__ DocSpan of_warp(int i, int* m) const {
-    if (!cu) {
-      *m = 0;
-      return DocSpan{0, N, 0};
-    }
-    *m = find_warp(i);
-    return span(*m, i);
-  }
-  // The document of this thread's row i, known to be one of mlo..mhi.
-  __device__ __forceinline__ DocSpan of_thread(int i, int mlo, int mhi) const {
-    if (!cu) return DocSpan{0, N, 0};
-    mlo = mlo < 0 ? 0 : mlo;
-    mhi = mhi > n - 1 ? n - 1 : mhi;
-    while (mlo < mhi) {
-      const int mid = (mlo + mhi + 1) >> 1;
-      if (__ldg(cu + mid) <= i) mlo = mid;
-      else mhi = mid - 1;
-    }
-    return span(mlo, i);
-  }
+  __device__ __forceinline__ DocSpan of_thread(const DocTiles& t, int i) const;
   // First and last key of row i of document s (none: 1, 0).
   __device__ __forceinline__ int key_first(const DocSpan& s, int i) const {
     if (s.start >= s.end) return 1;
@@ -144,22 +156,74 @@ struct DocTiles {
   int int_lo, int_hi;    // tiles that need no element mask (lo > hi: none)
   int mlo, mhi;          // documents of the rows
   int c0, cn;            // rows outside [c0, cn) are padding
+  // boundary base + lane and its document's prefix length, held by each lane
+  int base, bound, pre;
 };
 
+// Makes span and of_thread of a warp's lanes (see DocTiles::bound).
+__device__ __forceinline__ DocSpan span_of_lanes(const DocTiles& t, int n, int m, int i) {
+  const int k = m - t.base;
+  const int a = __shfl_sync(0xffffffffu, t.bound, k & 31);
+  const int e = __shfl_sync(0xffffffffu, t.bound, (k + 1) & 31);
+  const int len = __shfl_sync(0xffffffffu, t.pre, k & 31);
+  DocSpan s{0, 0, 0};
+  if (m < 0 || m >= n || i < a || i >= e) return s;
+  s.start = a;
+  s.end = e;
+  s.pre = len >= e - a ? e : a + (len < 0 ? 0 : len);
+  return s;
+}
+
+// By a whole converged warp (every warp of the block computes it for itself).
+// With at most 31 documents all boundaries come in one load and the rest is
+// warp votes and shuffles; otherwise the first row's document is searched
+// for, and the 31 documents from there on are held (a tile's rows beyond
+// them, tiny documents, are looked up in memory).
 template <bool kQueriesOfKeys>
 __device__ __forceinline__ DocTiles doc_tiles(const DocMask& dm, int m0, int m1) {
+  const int lane = threadIdx.x & 31;
   DocTiles t;
-  t.c0 = dm.first();
-  t.cn = dm.past();
   t.begin = t.end = 0;
   t.int_lo = 1;
   t.int_hi = 0;
   t.mlo = 0;
   t.mhi = -1;
-  const int r0 = m0 > t.c0 ? m0 : t.c0;
-  const int r1 = m1 < t.cn - 1 ? m1 : t.cn - 1;
+  t.base = 0;
+  t.bound = 0;
+  t.pre = 0;
+  DocSpan s0{0, dm.N, 0}, s1{0, dm.N, 0};
+  int r0 = m0, r1 = m1;
+  t.c0 = 0;
+  t.cn = dm.N;
+  if (dm.cu) {
+    const bool few = dm.n <= 31;
+    if (!few) {
+      t.c0 = dm.first();
+      t.cn = dm.past();
+      t.base = dm.find_warp(m0 > t.c0 ? m0 : t.c0);
+      t.base = t.base < 0 ? 0 : (t.base > dm.n ? dm.n : t.base);
+    }
+    const int at = t.base + lane;
+    t.bound = at <= dm.n ? dm.clampN(__ldg(dm.cu + at)) : 0x7fffffff;
+    if (dm.pre && at < dm.n) t.pre = __ldg(dm.pre + at);
+    if (few) {
+      t.c0 = __shfl_sync(0xffffffffu, t.bound, 0);
+      t.cn = __shfl_sync(0xffffffffu, t.bound, dm.n);
+    }
+    r0 = m0 > t.c0 ? m0 : t.c0;
+    r1 = m1 < t.cn - 1 ? m1 : t.cn - 1;
+    if (r0 > r1) return t;
+    t.mlo = t.base + __popc(__ballot_sync(0xffffffffu, t.bound <= r0)) - 1;
+    t.mhi = t.base + __popc(__ballot_sync(0xffffffffu, t.bound <= r1)) - 1;
+    s0 = span_of_lanes(t, dm.n, t.mlo, r0);
+    if (t.mhi - t.base < 31) {
+      s1 = span_of_lanes(t, dm.n, t.mhi, r1);
+    } else {
+      t.mhi = dm.find_warp(r1);
+      s1 = dm.span(t.mhi, r1);
+    }
+  }
   if (r0 > r1) return t;
-  const DocSpan s0 = dm.of_warp(r0, &t.mlo), s1 = dm.of_warp(r1, &t.mhi);
   const int a0 = kQueriesOfKeys ? dm.query_first(s0, r0) : dm.key_first(s0, r0);
   const int b1 = kQueriesOfKeys ? dm.query_last(s1, r1) : dm.key_last(s1, r1);
   if (a0 > b1) return t;
@@ -172,6 +236,25 @@ __device__ __forceinline__ DocTiles doc_tiles(const DocMask& dm, int m0, int m1)
     t.int_hi = (b + 1) / kTileN - 1;
   }
   return t;
+}
+
+// The document of this thread's row i, one of the rows of t (a whole
+// converged warp; other rows get none or a document that does not hold them).
+__device__ __forceinline__ DocSpan DocMask::of_thread(const DocTiles& t, int i) const {
+  if (!cu) return DocSpan{0, N, 0};
+  int mlo = t.mlo < 0 ? 0 : t.mlo, mhi = t.mhi > n - 1 ? n - 1 : t.mhi;
+  if (mhi - t.base < 31) {
+    int m = mlo;
+    for (int k = mlo + 1; k <= mhi; ++k)
+      if (i >= __shfl_sync(0xffffffffu, t.bound, k - t.base)) m = k;
+    return span_of_lanes(t, n, m, i);
+  }
+  while (mlo < mhi) {
+    const int mid = (mlo + mhi + 1) >> 1;
+    if (__ldg(cu + mid) <= i) mlo = mid;
+    else mhi = mid - 1;
+  }
+  return span(mlo, i);
 }
 
 }  // namespace swa

@@ -1,7 +1,6 @@
 """Host checks of the operators with shaped scores, of the shared-prefix decode and of
 the rotated paged append: what the C entries and the binding refuse (no GPU call is
 reached), the order of the arguments they hand on, and the 64-bit reference itself."""
-import contextlib
 import ctypes
 import math
 
@@ -135,10 +134,9 @@ def lib(monkeypatch):
     rec = Recorder()
     monkeypatch.setattr(b, "_lib", rec)
     monkeypatch.setattr(b, "_placed", lambda ref, **kw: None)
-    monkeypatch.setattr(b, "_token_rows", lambda x, n, ref: x.stride(0))
+    monkeypatch.setattr(b, "_token_rows", lambda x, n, dev: x.stride(0))
     monkeypatch.setattr(b, "_stream", lambda s: "STREAM")
-    monkeypatch.setattr(b, "_on_stream", lambda s: contextlib.nullcontext())
-    monkeypatch.setattr(b.torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(b.torch.cuda, "current_device", lambda: -1)  # what CPU tensors say
     return rec
 
 
@@ -233,22 +231,22 @@ def test_binding_refuses_shapes(lib):
 
 def test_binding_checks_token_strides():
     class OnGpu:  # a CUDA tensor's shape and strides without a GPU
-        is_cuda, device = True, "cuda:0"
-
         def __init__(self, shape, stride):
             self.shape, self._s = shape, stride
 
-        def stride(self, i):
-            return self._s[i]
-    ref = OnGpu((1, 1, 1), (1, 1, 1))
-    assert b._token_rows(OnGpu((4, 2, 64), (512, 64, 1)), "q", ref) == 512
-    assert b._token_rows(OnGpu((1, 2, 64), (7, 64, 1)), "q", ref) == 128  # one token: any stride
-    assert b._token_rows(OnGpu((4, 1, 64), (512, 3, 1)), "q", ref) == 512
+        def get_device(self):
+            return 0
+
+        def stride(self):
+            return self._s
+    assert b._token_rows(OnGpu((4, 2, 64), (512, 64, 1)), "q", 0) == 512
+    assert b._token_rows(OnGpu((1, 2, 64), (7, 64, 1)), "q", 0) == 128  # one token: any stride
+    assert b._token_rows(OnGpu((4, 1, 64), (512, 3, 1)), "q", 0) == 512
     for s in ((512, 64, 2), (512, 128, 1), (64, 64, 1), (0, 64, 1)):
         with pytest.raises(ValueError):
-            b._token_rows(OnGpu((4, 2, 64), s), "q", ref)
+            b._token_rows(OnGpu((4, 2, 64), s), "q", 0)
     with pytest.raises(ValueError, match="CUDA"):
-        b._token_rows(t(4, 2, 64), "q", ref)
+        b._token_rows(t(4, 2, 64), "q", 0)
 
 
 def test_empty_calls_check_their_tensors():
