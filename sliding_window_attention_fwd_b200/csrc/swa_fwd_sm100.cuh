@@ -823,43 +823,31 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       }
       tmem_wait_ld();
     };
-    // Shaped scores: the 64 raw products of key half hf of tile it become
-    // score - m_ref in log2 units.  The cap is s * q(s^2), so its last
-    // multiplication takes the subtraction of m_ref (and the bias) with it.
-    // The bias is linear in the key while a half lies on one side of every
-    // row of the warp; only halves on the diagonal need |i - j| per key.
-    auto shape_half = [&](int it, int hf, float (&sv)[64], float m_ref) {
-      float2 add0 = make_float2(-m_ref, -m_ref);  // of keys 0 and 1
-      float2 step = make_float2(0.f, 0.f);        // per two keys
-      bool diag = false;
-      float base = 0.f;
+    // Shaped scores: the raw products of a key half become score - m_ref in
+    // log2 units.  The cap is s * q(s^2), so its last multiplication takes the
+    // subtraction of m_ref (and the bias) with it.  The bias is linear in the
+    // key while a half lies on one side of every row of the warp; only halves
+    // on the diagonal need |i - j| per key.
+    struct HalfShape {
+      float add, k1, base;  // addend of key j: add + k1 j, or -m_ref + nslope2 |base - j|
+      bool diag, small;
+    };
+    auto half_shape = [&](int it, int hf, const float (&sv)[64], float m_ref) -> HalfShape {
+      HalfShape q;
+      q.add = -m_ref;
+      q.k1 = q.base = 0.f;
+      q.diag = false;
+      q.small = true;
       if (bias_on) {
         const int n0 = (tr.kv_begin + it) * kTileN + hf * 64;
-        int lo, hi;  // rows of the warp, relative to the half's first key
-        if (shared) {
-          lo = 64;  // keys of a prefix never lie behind a row that sees them
-          hi = 64;
-          base = (float)(pos_q - n0);
-        } else {
-          lo = m_v - lane - n0;
-          hi = lo + 31;
-          base = (float)(m_v - n0);
-        }
-        diag = lo < 63 && hi > 0;
-        const float k1 = lo >= 63 ? -nslope2 : nslope2;  // per key
-        add0.x = fmaf(-k1, base, -m_ref);
-        add0.y = add0.x + k1;
-        step = make_float2(2.f * k1, 2.f * k1);
+        // rows of the warp relative to the half's first key (keys of a shared
+        // prefix never lie behind a row that sees them)
+        const int lo = shared ? 64 : m_v - lane - n0, hi = lo + 31;
+        q.base = shared ? (float)(pos_q - n0) : (float)(m_v - n0);
+        q.diag = lo < 63 && hi > 0;
+        q.k1 = lo >= 63 ? -nslope2 : nslope2;
+        if (!q.diag) q.add = fmaf(-q.k1, q.base, -m_ref);
       }
-      // addend of keys 2e and 2e + 1
-      auto addend = [&](int e) -> float2 {
-        if (!bias_on) return add0;
-        if (diag) {
-          return make_float2(fmaf(nslope2, fabsf(base - (float)(2 * e)), -m_ref),
-                             fmaf(nslope2, fabsf(base - (float)(2 * e + 1)), -m_ref));
-        }
-        return fma2(make_float2((float)e, (float)e), step, add0);
-      };
       if (cap_on) {
         float t[4];
 #pragma unroll
@@ -871,29 +859,40 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], fabsf(sv[60 + e]));
         const float big = max3f(t[0], t[1], fmaxf(t[2], t[3]));
-        if (!__any_sync(0xffffffffu, big > p.cap.small)) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 x = cap_small(p.cap, make_float2(sv[2 * e], sv[2 * e + 1]), addend(e));
-            sv[2 * e] = x.x;
-            sv[2 * e + 1] = x.y;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 x = cap_any(p.cap, make_float2(sv[2 * e], sv[2 * e + 1]), addend(e));
-            sv[2 * e] = x.x;
-            sv[2 * e + 1] = x.y;
-          }
-        }
-      } else {
-        const float2 sl2_2 = make_float2(sl2, sl2);
+        q.small = !__any_sync(0xffffffffu, big > p.cap.small);
+      }
+      return q;
+    };
+    // Keys 2e and 2e + 1 of the half; kLinear: not on the diagonal.
+    auto shape_pair = [&](const HalfShape& q, int e, float2 s, auto is_small,
+                          auto is_linear) -> float2 {
+      float2 add = make_float2(q.add, q.add);
+      if (bias_on) {
+        if (decltype(is_linear)::value)
+          add = make_float2(fmaf(q.k1, (float)(2 * e), q.add), fmaf(q.k1, (float)(2 * e + 1), q.add));
+        else
+          add = make_float2(fmaf(nslope2, fabsf(q.base - (float)(2 * e)), q.add),
+                            fmaf(nslope2, fabsf(q.base - (float)(2 * e + 1)), q.add));
+      }
+      if (!cap_on) return fma2(s, make_float2(sl2, sl2), add);
+      return decltype(is_small)::value ? cap_small(p.cap, s, add) : cap_any(p.cap, s, add);
+    };
+    auto shape_half = [&](const HalfShape& q, float (&sv)[64]) {
+      auto run = [&](auto is_small, auto is_linear) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 x = fma2(make_float2(sv[2 * e], sv[2 * e + 1]), sl2_2, addend(e));
+          const float2 x =
+              shape_pair(q, e, make_float2(sv[2 * e], sv[2 * e + 1]), is_small, is_linear);
           sv[2 * e] = x.x;
           sv[2 * e + 1] = x.y;
         }
+      };
+      if (bias_on && q.diag) {
+        if (q.small) run(std::true_type(), std::false_type());
+        else run(std::false_type(), std::false_type());
+      } else {
+        if (q.small) run(std::true_type(), std::true_type());
+        else run(std::false_type(), std::true_type());
       }
     };
     // zeros over the V rows of tile it outside [z0, z1) (thread r: row r), so
@@ -990,17 +989,25 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
         tmem_st16(tS + pcol + jj * 16, pk);
       }
     };
-    // The same for shaped scores, whose maximum is already taken off: 2^(sv +
-    // d).  The pairs on the FMA pipe take the finer polynomial (2.6e-6), so
-    // that lse keeps fp32 accuracy.
-    auto exp_shaped = [&](int pcol, const float (&sv)[64], float d, float2 (&ls)[4]) {
+    // The same for shaped scores, whose maximum is already taken off.  raw: sv
+    // holds the raw products still (linear bias, cap in its usual range) and
+    // is shaped on the way, so that the FMA pipe works on some keys while MUFU
+    // works on others.  The pairs on the FMA pipe take the finer polynomial
+    // (2.6e-6), so that lse keeps fp32 accuracy.
+    auto exp_shaped = [&](int pcol, float (&sv)[64], float2 (&ls)[4], const HalfShape& q,
+                          auto raw) {
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 xa =
-              add2(make_float2(sv[jj * 32 + 2 * e], sv[jj * 32 + 2 * e + 1]), make_float2(d, d));
+          const int c = jj * 16 + e;
+          float2 xa = make_float2(sv[2 * c], sv[2 * c + 1]);
+          if (decltype(raw)::value) {
+            xa = shape_pair(q, c, xa, std::true_type(), std::true_type());
+            sv[2 * c] = xa.x;
+            sv[2 * c + 1] = xa.y;
+          }
           float2 pr;
           if (D != 64 && (e & 7) == 7) {
             pr = exp2_poly2_fine(xa);
@@ -1089,19 +1096,37 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       float sv[64];
 
       if constexpr (scored) {
-        // One half: scores against the running maximum m_used (0 while the
-        // row has no key), P, and the half's maximum.  late: O must hold the
-        // early half's PV before it is scaled.
+        // The early half, then the late one (one body, so that the loop stays
+        // small): scores against the running maximum m_used (0 while the row
+        // has no key), P, and the half's maximum.
         float tmax = -INFINITY;  // of the tile
-        auto half = [&](int hf, int pcol, bool late) -> bool {
+#pragma unroll 1
+        for (int late = 0; late < 2; ++late) {
+          const int hf = e ^ late, pcol = 64 * e + 32 * late;
+          const bool w_ok =
+              mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
+          if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
+          tc_fence_after();
+          read_half(hf, sv);
+          if (late) {
+            // these columns now belong to the early half of the next tile
+            tc_fence_before();
+            mbar_arrive(&l_free[slot]);
+          }
           const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-          shape_half(it, hf, sv, m_ref);
-          mask_half(it, hf, edge, sv);
+          const HalfShape q = half_shape(it, hf, sv, m_ref);
           const bool first = __any_sync(0xffffffffu, m_used == -INFINITY);
           float2 lh[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
-          // optimistic: P is formed while the half's maximum is found
-          if (!first) exp_shaped(pcol, sv, 0.f, lh);
+          // the usual half, with no key to mask: P is formed while the half's
+          // maximum is found; otherwise the maximum comes first
+          const bool usual = !first && !q.diag && q.small && !__any_sync(0xffffffffu, edge);
+          if (usual) {
+            exp_shaped(pcol, sv, lh, q, std::true_type());
+          } else {
+            shape_half(q, sv);
+            mask_half(it, hf, edge, sv);
+          }
           const float hmax = half_max(sv);  // above m_ref
           tmax = fmaxf(tmax, m_ref + hmax);
           const bool adopt = m_used == -INFINITY;
@@ -1111,10 +1136,11 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
           if (any_jump) {
             const float m_old = m_used;
             if (late) {
+              // O must hold the early half's PV before it is scaled
               const bool oe_ok = mbar_wait(&oe_done[slot], (uint32_t)it & 1u, p.err, abort_flag);
-              if (!__all_sync(0xffffffffu, oe_ok)) return false;
+              if (!__all_sync(0xffffffffu, oe_ok)) { ok = false; break; }
             }
-            if (!rescale_o(it, jump, m_ref + hmax)) return false;
+            if (!rescale_o(it, jump, m_ref + hmax)) { ok = false; break; }
             const float f = jump ? ex2_approx(m_old - m_used) : 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1123,33 +1149,22 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
             }
             tmem_wait_st();
           }
-          if (first || any_jump)
-            exp_shaped(pcol, sv, m_used == -INFINITY ? 0.f : m_ref - m_used, lh);
+          if (!usual || any_jump) {
+            const float d = m_used == -INFINITY ? 0.f : m_ref - m_used;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] += d;
+            exp_shaped(pcol, sv, lh, q, std::false_type());
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) ls[j] = add2(ls[j], lh[j]);
-          return true;
-        };
-        bool w_ok = mbar_wait(&se_full[slot], ph, p.err, abort_flag);
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        tc_fence_after();
-        read_half(e, sv);
-        if (!half(e, 64 * e, false)) { ok = false; break; }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&pe_full[slot]);
-        w_ok = mbar_wait(&sl_full[slot], ph, p.err, abort_flag);
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        tc_fence_after();
-        read_half(e ^ 1, sv);
-        // these columns now belong to the early half of the next tile
-        tc_fence_before();
-        mbar_arrive(&l_free[slot]);
-        if (!half(e ^ 1, 64 * e + 32, true)) { ok = false; break; }
+          tmem_wait_st();
+          tc_fence_before();
+          if (!late) mbar_arrive(&pe_full[slot]);
+        }
+        if (!ok) break;
         const float2 a2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
         l += a2.x + a2.y;
         if (tmax > m_used + kRescaleThreshold) m_pend = tmax;
-        tmem_wait_st();
-        tc_fence_before();
         mbar_arrive(&p_full[slot]);
         continue;
       }
