@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -629,6 +630,12 @@ def swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail) -> in
     return _lib.swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail)
 
 
+@functools.lru_cache(maxsize=256)
+def _shared_workspace(dev, *sizes):
+    with torch.cuda.device(dev):
+        return _lib.swa_decode_shared_workspace_bytes(*sizes)
+
+
 def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, pos, page_size, W,
                       out=None, lse=None, keep_prefix=True, max_tail=None, softcap=0.0,
                       slopes=None, scale=0.0, stream=None):
@@ -674,11 +681,7 @@ def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, 
     if max_tail is None:
         max_tail = max_pages * page_size - n_prefix
     max_tail = max(0, min(max_tail, 2 ** 31 - 1))
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            nbytes = _lib.swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail)
-    else:
-        nbytes = _lib.swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail)
+    nbytes = _shared_workspace(dev, B, H, Hkv, D, n_prefix, W, max_tail)
     ws = _scratch(max(16, nbytes), torch.uint8, q.device, stream)
     _run(dev, stream, "swa_decode_shared", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
          out.data_ptr(), _at(lse), prefix_table.data_ptr() if n_prefix else None, n_prefix,

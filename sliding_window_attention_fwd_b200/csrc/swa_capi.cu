@@ -529,7 +529,7 @@ SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_
   // (rows of the pool are 32-bit coordinates of a TMA box)
   if (H / Hkv > 8 || page_size % kBlockRows != 0 ||
       (int64_t)num_pages * page_size > 0x7fffffffLL ||
-      (int64_t)B * (H / Hkv) > 0x7fffffffLL - 2 * kTileM || n_prefix > 0x7fffffff - 2 * kTileN)
+      (int64_t)B * H > 0x7fffffffLL - 2 * kTileM || n_prefix > 0x7fffffff - 2 * kTileN)
     return SWA_ERR_UNSUPPORTED;
   if (B == 0) return SWA_OK;
   const SharedPlan pl = shared_plan(B, H, Hkv, D, n_prefix, W, max_tail);

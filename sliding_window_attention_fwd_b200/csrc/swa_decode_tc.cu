@@ -34,7 +34,6 @@
 
 #include "swa_internal.h"
 #include "swa_ptx.cuh"
-#include "swa_score.cuh"
 
 namespace swa {
 namespace {
@@ -43,6 +42,7 @@ constexpr int kTK = 128;        // keys per tile (MMA M)
 constexpr int kPart = 1024;     // key indices per CTA, about
 constexpr int kNQ = 8;          // query vectors of a GQA group, at most
 constexpr int kN = 16;          // MMA N: the group padded with zero rows
+constexpr int kRingSlots = 3;   // TMA ring (each slot one K or one V tile)
 constexpr int kDecChunk = kTK * 128;  // one 64-column slice of a 128-row tile (bytes)
 constexpr float kLazy = 8.0f;   // log2 units
 
@@ -62,31 +62,18 @@ struct DecParams {
   int B, H, Hkv, W, grp, nsplit;
   int part_keys;  // key indices per CTA (a multiple of 128)
   float scale_log2;
-  // behind a shared prefix: only positions >= n_prefix, the last part takes
-  // every key left, a negative position is an inactive sequence; the cap, and
-  // slopes [H] of the distance bias (NULL: none)
-  int n_prefix, num_pages;
-  CapCoefs cap;
-  const float* slopes;
 };
 
-// D = 128 (the head size of the ring-decode workload); D = 64 behind a shared
-// prefix only.  O^T = V^T P^T keeps M = 128 at D = 64: rows 64-127 of its A
-// operand are whatever follows the V tile in shared memory (the next ring
-// slot, or the pad behind the last one) and rows 64-127 of O^T, which nobody
-// reads, what comes of it.
-template <int D_>
-struct DecCfgT {
-  static constexpr int D = D_;
-  static constexpr int kTile = kTK * D * 2;       // 32 KB at D = 128: one K or V tile
-  static constexpr int kRingSlots = D == 128 ? 3 : 5;  // TMA ring (each slot one K or one V tile)
-  static constexpr int kPad = D == 128 ? 0 : kTK * 128;
+// D = 128 (the head size of the ring-decode workload).
+struct DecCfg {
+  static constexpr int D = 128;
+  static constexpr int kTile = kTK * D * 2;       // 32 KB: one K or V tile
   static constexpr int kQ = 0;                    // Q: 16 rows x D, two 2 KB slices
   static constexpr int kQBytes = kN * D * 2;      // 4 KB
   static constexpr int kP = kQ + kQBytes;         // P^T: 16 rows x 128 keys, two 2 KB slices
   static constexpr int kPBytes = kN * kTK * 2;    // 4 KB, two buffers
   static constexpr int kRing = kP + 2 * kPBytes;  // 12 KB (1024-aligned)
-  static constexpr int kBar = kRing + kRingSlots * kTile + kPad;
+  static constexpr int kBar = kRing + kRingSlots * kTile;
   // full[S], empty[S], s_full[2], p_full[2], o_done[2], o_final
   static constexpr int kNumBars = 2 * kRingSlots + 7;
   static constexpr int kRed = kBar + kNumBars * 8;  // per-warp partial max / sum: 4 x kNQ floats
@@ -98,7 +85,6 @@ struct DecCfgT {
   static_assert(kRing % 1024 == 0, "ring alignment");
   static_assert(2 * (kAlloc + 1024) <= 233472, "two CTAs per SM");
 };
-using DecCfg = DecCfgT<128>;
 
 // byte offset of element (row, col) in a 128-byte-swizzled K-major operand
 // of 16 rows, 64 columns per 2 KB slice
@@ -107,12 +93,10 @@ __device__ __forceinline__ uint32_t sw128_off16(int row, int col) {
   return (uint32_t)(slice * 2048 + row * 128 + ((((c >> 3) ^ (row & 7)) & 7) << 4) + ((c & 7) << 1));
 }
 
-// kOwn: the own keys of a decode behind a shared prefix (paged).
-template <int D, bool kOwn>
-__global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
+__global__ void __launch_bounds__(DecCfg::kThreads, 2)
     swa_decode_tc_kernel(const __grid_constant__ DecParams p) {
-  using C = DecCfgT<D>;
-  constexpr int kRingSlots = C::kRingSlots;
+  using C = DecCfg;
+  constexpr int D = C::D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -142,20 +126,16 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
   // the positions below a masked
   long long a64 = 0;
   int lo_idx = 0, n_idx;
-  if (kOwn || p.paged) {
-    long long a = pb - p.W + 1 > 0 ? pb - p.W + 1 : 0;
-    if (kOwn && a < p.n_prefix) a = p.n_prefix;
+  if (p.paged) {
+    const long long a = pb - p.W + 1 > 0 ? pb - p.W + 1 : 0;
     a64 = a & ~63LL;
     lo_idx = (int)(a - a64);
-    // (own keys: of the positions the block table covers)
-    long long last = pb;
-    if (kOwn) last = min(last, (long long)p.max_pages * p.page_size - 1);
-    n_idx = kOwn && last < a ? 0 : (int)(last - a64 + 1);
+    n_idx = (int)(pb - a64 + 1);
   } else {
     n_idx = pb + 1 < (long long)p.W ? (int)(pb + 1) : p.W;  // filled slots
   }
   const int s0 = part * p.part_keys;
-  const int s1 = kOwn && part == p.nsplit - 1 ? n_idx : min(s0 + p.part_keys, n_idx);
+  const int s1 = min(s0 + p.part_keys, n_idx);
   const int ntiles = s1 > s0 ? (s1 - s0 + kTK - 1) / kTK : 0;
   const int nq = p.grp;
 
@@ -178,12 +158,11 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
       // below)
       const int idx0 = s0 + t * kTK + hh * 64;
       int row = idx0, bc = b;
-      if (kOwn || p.paged) {
+      if (p.paged) {
         const long long t0 = a64 + idx0;
         const long long lp = t0 / p.page_size;
-        const long long page =
-            lp < p.max_pages && !(kOwn && idx0 >= s1) ? p.table[(long)b * p.max_pages + lp] : -1;
-        row = page < 0 || (kOwn && page >= p.num_pages) ? -64 : (int)(page * p.page_size + t0 % p.page_size);
+        const long long page = lp < p.max_pages ? p.table[(long)b * p.max_pages + lp] : -1;
+        row = page < 0 ? -64 : (int)(page * p.page_size + t0 % p.page_size);
         bc = 0;
       }
       for (int cc = 0; cc < D / 64; ++cc)
@@ -266,7 +245,7 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
     // buffer of tile t - 1, whose P^T the issuer has already waited for.
     if (lane == 0 && ntiles > 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kTK, kN, 0, 0);  // K-major A (K), K-major B (Q)
-      const uint32_t idesc_o = idesc_bf16_f32(128, kN, 1, 0);  // MN-major A (V^T), K-major B (P^T)
+      const uint32_t idesc_o = idesc_bf16_f32(D, kN, 1, 0);    // MN-major A (V^T), K-major B (P^T)
       const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
       const uint64_t dp0 = sdesc_sw128(smem_u32(smem + C::kP), 16, 1024);
       const uint64_t dring_k = sdesc_sw128(ring_addr, 16, 1024);
@@ -324,34 +303,8 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
       lsum[n] = 0.f;
     }
     bool ok = true;
-    float nslope2[kNQ];
-    if (kOwn) {
-#pragma unroll
-      for (int n = 0; n < kNQ; ++n)
-        nslope2[n] = p.slopes && n < nq
-                         ? -__ldg(p.slopes + g * p.grp + n) * 1.4426950408889634f
-                         : 0.f;
-    }
     for (int t = 0; t < ntiles; ++t) {
-      bool w_ok = true;
-      if (kOwn) {
-        // keys of the tile outside the sequence's own (pool rows not yet
-        // written, or another's) may hold anything, NaN included: their V
-        // rows become zeros before P = 0 meets them
-        const int j = s0 + t * kTK + r;
-        if (s0 + t * kTK < lo_idx || s0 + t * kTK + kTK > s1) {
-          const int jv = 2 * t + 1, st = jv % kRingSlots;
-          w_ok = mbar_wait(&full[st], (uint32_t)(jv / kRingSlots) & 1u, p.err, abort_flag);
-          if (w_ok && (j < lo_idx || j >= s1)) {
-            uint8_t* vt = smem + C::kRing + st * C::kTile + r * 128;
-#pragma unroll 1
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<uint4*>(vt + (i / 8) * kDecChunk + (i % 8) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-      }
-      w_ok = mbar_wait(&s_full[t & 1], (uint32_t)(t >> 1) & 1u, p.err, abort_flag) && w_ok;
+      bool w_ok = mbar_wait(&s_full[t & 1], (uint32_t)(t >> 1) & 1u, p.err, abort_flag);
       tc_fence_after();
       uint32_t sv[16];
       tmem_ld16(tmem + 16u * (t & 1) + lane_off, sv);
@@ -359,18 +312,8 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
       const int idx = s0 + t * kTK + r;
       const bool valid = idx < s1 && idx >= lo_idx;
       float xs[kNQ];
-      if (kOwn && (p.cap.out > 0.f || p.slopes)) {
-        const float dist = (float)(pb - a64 - idx);
 #pragma unroll
-        for (int n = 0; n < kNQ; ++n) {
-          float x = __uint_as_float(sv[n]);
-          x = p.cap.out > 0.f ? tanh_any(p.cap, x) * p.cap.out : x * sl2;
-          xs[n] = valid ? fmaf(nslope2[n], dist, x) : -INFINITY;
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) xs[n] = valid ? __uint_as_float(sv[n]) * sl2 : -INFINITY;
-      }
+      for (int n = 0; n < kNQ; ++n) xs[n] = valid ? __uint_as_float(sv[n]) * sl2 : -INFINITY;
       // tile max per query: the warp, then the four warps
 #pragma unroll
       for (int n = 0; n < kNQ; ++n) {
@@ -460,10 +403,7 @@ __global__ void __launch_bounds__(DecCfgT<D>::kThreads, 2)
       tmem_ld16(tmem + 32u + lane_off, ov);
       tmem_wait_ld();
       for (int n = 0; n < nq; ++n) {
-        if (D == 128 || r < D)
-          p.part_o[(rowbase + n) * D + r] = kOwn && l_tot[n] == 0.f
-                                                ? 0.f
-                                                : __uint_as_float(ov[n]) / l_tot[n];
+        p.part_o[(rowbase + n) * D + r] = __uint_as_float(ov[n]) / l_tot[n];
         if (r == 0) p.part_lse[rowbase + n] = (m_run[n] + __log2f(l_tot[n])) * 0.69314718055994531f;
       }
     }
@@ -489,7 +429,7 @@ namespace {
 int launch_tc(DecParams& p, const void* q, void* out, float* lse, const int64_t* pos, int B,
               int H, int Hkv, int D, int W, int span, float scale, cudaStream_t stream) {
   static std::atomic<unsigned long long> attr{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_decode_tc_kernel<128, false>), DecCfg::kAlloc, attr))
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_decode_tc_kernel), DecCfg::kAlloc, attr))
     return SWA_ERR_CUDA;
   // about kPart keys per CTA: as many parts as W needs, the span (W, or
   // W + 63 from a 64-aligned start) shared evenly in whole 128-key tiles
@@ -513,8 +453,7 @@ int launch_tc(DecParams& p, const void* q, void* out, float* lse, const int64_t*
   p.scale_log2 = scale * 1.4426950408889634f;
   const long long grid = (long long)B * Hkv * p.nsplit;
   if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
-  swa_decode_tc_kernel<128, false>
-      <<<(unsigned)grid, DecCfg::kThreads, DecCfg::kAlloc, stream>>>(p);
+  swa_decode_tc_kernel<<<(unsigned)grid, DecCfg::kThreads, DecCfg::kAlloc, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
   return split_merge(part, out, lse, p.nsplit, B, 1, H, D, stream);
 }
@@ -552,57 +491,6 @@ int launch_decode_paged_tc(const void* q, const void* k_pages, const void* v_pag
   p.max_pages = max_pages;
   // the window's positions from a 64-aligned start: at most W + 63 indices
   return launch_tc(p, q, out, lse, pos, B, H, Hkv, D, W, W + 63, scale, stream);
-}
-
-namespace {
-template <int D>
-int launch_own_impl(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
-                    cudaStream_t stream) {
-  using C = DecCfgT<D>;
-  static std::atomic<unsigned long long> attr{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_decode_tc_kernel<D, true>), C::kAlloc,
-                      attr))
-    return SWA_ERR_CUDA;
-  DecParams p;
-  std::memset(&p, 0, sizeof(p));
-  const int pool_rows = a.num_pages * a.page_size;
-  if (encode_kv_map(&p.tmK, a.k_pages, D, a.Hkv, pool_rows, 1) != SWA_OK ||
-      encode_kv_map(&p.tmV, a.v_pages, D, a.Hkv, pool_rows, 1) != SWA_OK)
-    return SWA_ERR_CUDA;
-  p.q = static_cast<const uint16_t*>(a.q);
-  p.pos = a.pos;
-  p.table = a.table;
-  p.paged = 1;
-  p.page_size = a.page_size;
-  p.max_pages = a.max_pages;
-  p.num_pages = a.num_pages;
-  p.part_o = part_o;
-  p.part_lse = part_lse;
-  p.err = device_error_word();
-  if (!p.err) return SWA_ERR_CUDA;
-  p.B = a.B;
-  p.H = a.H;
-  p.Hkv = a.Hkv;
-  p.W = a.W;
-  p.grp = a.H / a.Hkv;
-  p.nsplit = pl.own_parts;
-  p.part_keys = pl.part_keys;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.n_prefix = a.n_prefix;
-  p.cap = cap_coefs(a.softcap, a.scale);
-  p.slopes = a.slopes;
-  const long long grid = (long long)a.B * a.Hkv * pl.own_parts;
-  if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;
-  swa_decode_tc_kernel<D, true><<<(unsigned)grid, C::kThreads, C::kAlloc, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
-}
-}  // namespace
-
-int launch_own(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
-               cudaStream_t stream) {
-  if (a.D == 128) return launch_own_impl<128>(a, pl, part_o, part_lse, stream);
-  if (a.D == 64) return launch_own_impl<64>(a, pl, part_o, part_lse, stream);
-  return SWA_ERR_UNSUPPORTED;
 }
 
 }  // namespace swa

@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   constexpr bool docs = KIND == 3;
   constexpr bool shared = KIND == 4;
   constexpr bool scored = docs || shared;
+  // the own keys' kernel reads nothing of this one's: it may start with it
+  if (shared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const bool gitem = glob && x < p.n_gitems;
   if (glob && !gitem) x -= p.n_gitems;
   int sp = 0;  // part of a split key walk
@@ -490,18 +492,25 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   if (shared && n_tiles > 0 && threadIdx.x >= 128) {
     // gather the item's query rows (zeros past the last) into the swizzled
     // layout of a TMA box
-    constexpr int kC16 = D / 8;
-    for (int idx = (int)threadIdx.x - 128; idx < NSLOT * kTileM * kC16; idx += 128 * NSLOT) {
-      const int row = idx / kC16, c16 = idx % kC16;
-      const int R = sr0 + row;
-      uint4 val = make_uint4(0u, 0u, 0u, 0u);
+    constexpr int kC16 = D / 8;  // 16-byte chunks per row; also rounds of the loop below
+    uint4 val[kC16];             // every load in flight at once
+#pragma unroll
+    for (int u = 0; u < kC16; ++u) {
+      const int idx = (int)threadIdx.x - 128 + u * 128 * NSLOT;
+      const int R = sr0 + idx / kC16, c16 = idx % kC16;
+      val[u] = make_uint4(0u, 0u, 0u, 0u);
       if (R < p.B * grp)
-        val = __ldg(reinterpret_cast<const uint4*>(
+        val[u] = __ldg(reinterpret_cast<const uint4*>(
             p.q_raw + ((size_t)(R / grp) * p.H + (size_t)g_kv * grp + R % grp) * D + c16 * 8));
+    }
+#pragma unroll
+    for (int u = 0; u < kC16; ++u) {
+      const int idx = (int)threadIdx.x - 128 + u * 128 * NSLOT;
+      const int row = idx / kC16, c16 = idx % kC16;
       const int rr = row % kTileM;
       uint8_t* d8 = smem + C::kQ + (row / kTileM) * C::kTile + (c16 / 8) * kChunkBytes + rr * 128 +
                     (((c16 % 8) ^ (rr % 8)) * 16);
-      *reinterpret_cast<uint4*>(d8) = val;
+      *reinterpret_cast<uint4*>(d8) = val[u];
     }
     fence_proxy_async_smem();
   }
@@ -1428,7 +1437,17 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
           for (int e = 0; e < 32; ++e) v[0][e] = v[1][e] = 0u;
         }
         if (split) {
-          if (row_valid) {
+          if (shared && row_valid && (reinterpret_cast<uintptr_t>(p.part_o) & 31u) == 0) {
+            // (whole 32-byte sectors)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              v[0][e] = __float_as_uint(__uint_as_float(v[0][e]) * inv);
+              v[1][e] = __float_as_uint(__uint_as_float(v[1][e]) * inv);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st_global_v8(p.part_o + prow * D + j2 * 64 + e * 8, &v[e >> 2][(e & 3) * 8]);
+          } else if (row_valid) {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + j2 * 64);
 #pragma unroll
             for (int e = 0; e < 16; ++e)

@@ -121,22 +121,24 @@ struct SharedArgs {
   int B, H, Hkv, D, page_size, num_pages, max_pages, n_prefix, W, keep, max_tail;
   float scale, softcap;
   const float* slopes;
+  const CUtensorMap* tmK;  // of the page pool (launch_decode_shared fills them in)
+  const CUtensorMap* tmV;
 };
 // How the keys of a call are split: parts of the prefix and of the own keys
 // (part_keys keys each, the last part taking what is left).
 struct SharedPlan {
-  int prefix_parts, own_parts, part_keys;
+  int prefix_parts, own_parts, part_keys, sms;
   size_t bytes;  // workspace: O / l and lse of every part
 };
 SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int max_tail);
-int launch_decode_shared(const SharedArgs& a, const SharedPlan& pl, void* workspace,
+int launch_decode_shared(SharedArgs a, const SharedPlan& pl, void* workspace,
                          cudaStream_t stream);
 // The prefix's share: parts 0 .. nsplit - 1 of the partial results.
 int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
                   cudaStream_t stream);
-// The own keys' share (swa_decode_tc.cu).
+// The own keys' share; behind: right behind launch_prefix on the stream.
 int launch_own(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
-               cudaStream_t stream);
+               bool behind, cudaStream_t stream);
 
 int launch_rope_append(const void* q, const void* k, const void* v, long long q_stride,
                        long long k_stride, long long v_stride, const float* inv_freq, int rot,

@@ -42,10 +42,8 @@ int launch(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
   p.nsplit = nsplit;
   p.part_o = part_o;
   p.part_lse = part_lse;
-  const int pool_rows = a.num_pages * a.page_size;
-  if (encode_kv_map(&p.tmK[0], a.k_pages, D, a.Hkv, pool_rows, 1) != SWA_OK ||
-      encode_kv_map(&p.tmV[0], a.v_pages, D, a.Hkv, pool_rows, 1) != SWA_OK)
-    return SWA_ERR_CUDA;
+  p.tmK[0] = *a.tmK;
+  p.tmV[0] = *a.tmV;
   const long long rows = (long long)a.B * (a.H / a.Hkv);
   const long long grid = (rows + NSLOT * kTileM - 1) / (NSLOT * kTileM) * a.Hkv * nsplit;
   if (grid > 0x7fffffffLL) return SWA_ERR_UNSUPPORTED;

@@ -791,8 +791,7 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const float* __restric
       for (int e = 0; e < kPer; ++e) acc[e] += w * f[e];
     }
   }
-  // (a row with no key in any part, an inactive sequence: zeros and lse -inf)
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = 1.f / wsum;
   uint16_t* dst = out + (((long long)b * C + c) * H + h) * D + lane * kPer;
   uint32_t pk[kPer / 2];
 #pragma unroll
