@@ -10,18 +10,18 @@
 // bytes behind them as rows 8-15, which fill columns that nobody reads.
 //
 // Tails are short (a few tiles), so a CTA per tail would spend most of its
-// time filling and draining.  The CTAs stay (two per SM) and walk the items
-// (part, kv head, sequence) i, i + grid, ...: the loads, the MMAs and the
-// softmax run on across item borders (Q, O^T and the item's lse double
-// buffered), so one item's last tiles overlap the next one's first loads.
-// Measured, 128 tails of 100 to 700 keys with 8 kv heads of 128 (210 MB): 70
-// us with a CTA per tail.
+// time filling and draining.  The CTAs stay (one per SM, six 32 KB tiles in
+// flight) and walk the items (part, kv head, sequence) i, i + grid, ...: the
+// loads, the MMAs and the softmax run on across item borders (Q and O^T
+// double buffered), and an item's result is written after the next one's
+// first tile.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer (and TMEM
 // owner), warps 2-5 softmax (thread r: key r of a tile, dimension r of O^T).
-// A tile is exponentiated against the running maximum unless some score
-// exceeds it by 2^8: one vote per tile, and only then the reduction over the
-// four warps.
+// The softmax of a tile is the chain that bounds a CTA, so it is kept short: a
+// tile is exponentiated against the running maximum unless some score exceeds
+// it by 2^8 (one vote per tile, and only then a reduction over the four
+// warps), and reductions of the group's values halve them at every shuffle.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,7 +37,7 @@ namespace swa {
 namespace {
 
 constexpr int kTK = 128;                // keys per tile (MMA M)
-constexpr int kNQ = 8;                  // query vectors of a GQA group, at most
+constexpr int kQRows = 8;               // rows of the query and P^T operands
 constexpr int kN = 16;                  // MMA N
 constexpr int kSlice = kTK * 128;       // one 64-column slice of a 128-row tile (bytes)
 constexpr float kLazy = 8.0f;           // log2 units
@@ -64,10 +64,10 @@ struct OwnParams {
 template <int D>
 struct OwnCfg {
   static constexpr int kTile = kTK * D * 2;            // one K or V tile
-  static constexpr int kSlots = D == 128 ? 3 : 5;      // ring of tiles
+  static constexpr int kSlots = D == 128 ? 6 : 11;     // ring of tiles
   static constexpr int kPad = D == 128 ? 0 : kSlice;
-  static constexpr int kQBytes = kNQ * D * 2;          // 8 rows, 1 KB per 64 columns
-  static constexpr int kPBytes = kNQ * kTK * 2;        // P^T: 8 rows x 128 keys
+  static constexpr int kQBytes = kQRows * D * 2;       // 8 rows, 1 KB per 64 columns
+  static constexpr int kPBytes = kQRows * kTK * 2;     // P^T: 8 rows x 128 keys
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kSlots * kTile + kPad;
   static constexpr int kP = kQ + 2 * kQBytes;
@@ -76,11 +76,11 @@ struct OwnCfg {
   // o_free[2], done
   static constexpr int kNumBars = 2 * kSlots + 13;
   static constexpr int kRed = kBar + kNumBars * 8;     // [2][warp][query] floats
-  static constexpr int kMisc = kRed + 2 * 4 * kNQ * 4;
+  static constexpr int kMisc = kRed + 2 * 4 * kQRows * 4;
   static constexpr int kAlloc = kMisc + 16 + 1024;     // slack for 1024-byte alignment
   static constexpr int kThreads = 192;
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand alignment");
-  static_assert(2 * (kAlloc + 1024) <= 233472, "two CTAs per SM");
+  static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
 // S^T buffers at columns 0 and 16, O^T at 32 and 48
@@ -104,6 +104,39 @@ __device__ __forceinline__ bool softmax_any(bool v) {
       : "r"((uint32_t)v)
       : "memory");
   return r != 0;
+}
+
+// Reduces kNQ values over the warp's 32 lanes: lane 16 b4 + 8 b3 + 4 b2 + ...
+// gets the one numbered by its upper bits (kNQ = 8: 4 b4 + 2 b3 + b2).
+template <int kNQ, class Op>
+__device__ __forceinline__ float reduce_values(const float (&v)[kNQ], Op op) {
+  static_assert(kNQ == 4 || kNQ == 8, "4 or 8 values");
+  const int lane = threadIdx.x & 31;
+  float a[kNQ];
+#pragma unroll
+  for (int n = 0; n < kNQ; ++n) a[n] = v[n];
+  int o = 16;
+#pragma unroll
+  for (int w = kNQ / 2; w > 0; w >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int n = 0; n < w; ++n) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? a[n] : a[n + w], o);
+      a[n] = op(up ? a[n + w] : a[n], other);
+    }
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+  return a[0];
+}
+// The value a lane gets, and whether it is the one to write it.
+template <int kNQ>
+__device__ __forceinline__ int reduced_index() {
+  return (threadIdx.x & 31) / (32 / kNQ);
+}
+template <int kNQ>
+__device__ __forceinline__ bool reduced_writer() {
+  return (threadIdx.x & (32 / kNQ - 1)) == 0;
 }
 
 // One item: part `part` of the own keys of sequence b for kv head g.  Keys
@@ -134,8 +167,8 @@ __device__ __forceinline__ Item item_of(const OwnParams& p, int i) {
   return t;
 }
 
-template <int D>
-__global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
+template <int D, int kNQ>
+__global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
     swa_own_kernel(const __grid_constant__ OwnParams p) {
   using C = OwnCfg<D>;
   constexpr int S_ = C::kSlots;
@@ -209,17 +242,21 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
                       t.b * p.H + t.g * p.grp, 0, 0);
         last_q = n_items++;
         const int32_t* table = p.table + (long long)t.b * p.max_pages;
+        // pages of tile k's two 64-row boxes (-1: read as zeros), looked up
+        // one tile ahead
+        auto page_at = [&](int k, int hh) -> int {
+          const int idx0 = t.s0 + k * kTK + hh * 64;
+          return idx0 < t.s1 ? __ldg(table + (t.a64 + idx0) / p.page_size) : -1;
+        };
+        int ahead[2] = {page_at(0, 0), page_at(0, 1)};
         for (int k = 0; ok && k < t.ntiles; ++k) {
-          int row[2];  // pool rows of the tile's two 64-row boxes (-64: zeros)
+          int row[2];
           for (int hh = 0; hh < 2; ++hh) {
-            const int idx0 = t.s0 + k * kTK + hh * 64;
-            row[hh] = -64;
-            if (idx0 < t.s1) {
-              const long long t0 = t.a64 + idx0;
-              const int page = __ldg(table + t0 / p.page_size);
-              if (page >= 0 && page < p.num_pages)
-                row[hh] = page * p.page_size + (int)(t0 % p.page_size);
-            }
+            row[hh] = ahead[hh] >= 0 && ahead[hh] < p.num_pages
+                          ? ahead[hh] * p.page_size +
+                                (int)((t.a64 + t.s0 + k * kTK + hh * 64) % p.page_size)
+                          : -64;
+            ahead[hh] = page_at(k + 1, hh);
           }
           for (int kv = 0; kv < 2; ++kv, ++j) {
             const int st = j % S_;
@@ -325,8 +362,41 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const int nq = p.grp;
     const size_t rows = (size_t)p.B * p.H;
+    const int my_n = reduced_index<kNQ>();
     bool ok = true;
     int tile = 0;  // over all items
+    // the item whose result is still to be written: its sums, first row and
+    // last tile
+    float m_last[kNQ], l_last[kNQ];
+    size_t row_last = 0;
+    int tile_last = -1;
+    // O / l and the lse of that item (the n-th): false when a wait gave up
+    auto finish = [&](int n_item) -> bool {
+      float* red_l = red + 4 * kNQ;
+      const float mine = reduce_values<kNQ>(l_last, [](float x, float y) { return x + y; });
+      if (reduced_writer<kNQ>()) red_l[wi * kNQ + my_n] = mine;
+      const bool w = mbar_wait(&o_done[tile_last & 1], (uint32_t)(tile_last >> 1) & 1u, p.err,
+                               abort_flag);
+      if (!bar_red_and(1, 128, w)) return false;
+      tc_fence_after();
+      uint32_t ov[16];
+      tmem_ld16(tmem + 32u + 16u * (n_item & 1) + lane_off, ov);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&o_free[n_item & 1]);
+#pragma unroll
+      for (int n = 0; n < kNQ; ++n) {
+        if (n < nq) {
+          const float l = red_l[n] + red_l[kNQ + n] + red_l[2 * kNQ + n] + red_l[3 * kNQ + n];
+          if (D == 128 || r < D)
+            p.part_o[(row_last + n) * D + r] =
+                l > 0.f ? __fdividef(__uint_as_float(ov[n]), l) : 0.f;
+          if (r == 0)
+            p.part_lse[row_last + n] = (m_last[n] + __log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      return true;
+    };
     for (int i = blockIdx.x; ok && i < p.items; i += step) {
       const Item t = item_of(p, i);
       const size_t row0 = (size_t)t.part * rows + (size_t)t.b * p.H + (size_t)t.g * nq;
@@ -345,20 +415,24 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
                          : 0.f;
       }
       for (int k = 0; k < t.ntiles; ++k, ++tile) {
-        const int idx = t.s0 + k * kTK + r;
+        const int k0 = t.s0 + k * kTK;  // the tile's first key
+        const int idx = k0 + r;
         const bool valid = idx < t.s1 && idx >= t.lo;
         bool w_ok = true;
-        if (t.s0 + k * kTK < t.lo || t.s0 + k * kTK + kTK > t.s1) {
+        if (k0 < t.lo || k0 + kTK > t.s1) {
           // rows of the pool that are not the sequence's may hold anything,
           // NaN included: their V rows become zeros before P = 0 meets them
           const int j = 2 * tile + 1, st = j % S_;
           w_ok = mbar_wait(&full[st], (uint32_t)(j / S_) & 1u, p.err, abort_flag);
-          if (w_ok && !valid) {
-            uint8_t* vt = smem + C::kRing + st * C::kTile + r * 128;
-#pragma unroll 1
-            for (int e = 0; e < D / 8; ++e)
-              *reinterpret_cast<uint4*>(vt + (e / 8) * kSlice + (e % 8) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+          constexpr int kC16 = D / 8;
+          const int below = t.lo > k0 ? t.lo - k0 : 0;
+          const int past = t.s1 - k0 < kTK ? t.s1 - k0 : kTK;
+          uint8_t* vt = smem + C::kRing + st * C::kTile;
+          for (int u = r; w_ok && u < (below + kTK - past) * kC16; u += 128) {
+            int row = u / kC16;
+            row = row < below ? row : row - below + past;
+            *reinterpret_cast<uint4*>(vt + (u % kC16 / 8) * kSlice + row * 128 + (u % 8) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
         }
         w_ok = mbar_wait(&s_full[tile & 1], (uint32_t)(tile >> 1) & 1u, p.err, abort_flag) && w_ok;
@@ -369,23 +443,39 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
         tmem_wait_ld();
         float xs[kNQ];
         const float dist = (float)(t.pos - t.a64 - idx);
+        if (p.cap.out > 0.f) {
+          float big = 0.f;
+#pragma unroll
+          for (int n = 0; n < kNQ; ++n) big = fmaxf(big, fabsf(__uint_as_float(sv[n])));
+          if (!__any_sync(0xffffffffu, valid && big > p.cap.small)) {
+#pragma unroll
+            for (int n = 0; n < kNQ; n += 2) {
+              const float2 x = cap_small(
+                  p.cap, make_float2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])),
+                  make_float2(nslope2[n] * dist, nslope2[n + 1] * dist));
+              xs[n] = x.x;
+              xs[n + 1] = x.y;
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kNQ; ++n)
+              xs[n] = fmaf(nslope2[n], dist, tanh_any(p.cap, __uint_as_float(sv[n])) * p.cap.out);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < kNQ; ++n)
+            xs[n] = fmaf(__uint_as_float(sv[n]), p.scale_log2, nslope2[n] * dist);
+        }
         bool grow = false;
 #pragma unroll
         for (int n = 0; n < kNQ; ++n) {
-          float x = __uint_as_float(sv[n]);
-          x = p.cap.out > 0.f ? tanh_any(p.cap, x) * p.cap.out : x * p.scale_log2;
-          xs[n] = valid && n < nq ? fmaf(nslope2[n], dist, x) : -INFINITY;
+          xs[n] = valid && n < nq ? xs[n] : -INFINITY;
           grow = grow || xs[n] > m_run[n] + kLazy;
         }
         // one vote per tile: the running maxima hold, or not
         if (softmax_any(grow || !w_ok)) {
-#pragma unroll
-          for (int n = 0; n < kNQ; ++n) {
-            float v = xs[n];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) red[wi * kNQ + n] = v;
-          }
+          const float mine = reduce_values<kNQ>(xs, [](float x, float y) { return fmaxf(x, y); });
+          if (reduced_writer<kNQ>()) red[wi * kNQ + my_n] = mine;
           // (all four warps leave together when a wait of one gave up)
           if (!bar_red_and(1, 128, w_ok)) {
             ok = false;
@@ -432,38 +522,25 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&p_full[tile & 1]);
-      }
-      // ---- the item's result: l over the 128 threads, then O / l
-      float* red_l = red + 4 * kNQ;
-#pragma unroll
-      for (int n = 0; n < kNQ; ++n) {
-        float v = lsum[n];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) red_l[wi * kNQ + n] = v;
-      }
-      ok = ok && mbar_wait(&o_done[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1u, p.err,
-                           abort_flag);
-      ok = bar_red_and(1, 128, ok);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t ov[16];
-      tmem_ld16(tO, ov);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(&o_free[n_items & 1]);
-      ++n_items;
-#pragma unroll
-      for (int n = 0; n < kNQ; ++n) {
-        if (n < nq) {
-          const float l =
-              red_l[n] + red_l[kNQ + n] + red_l[2 * kNQ + n] + red_l[3 * kNQ + n];
-          if (D == 128 || r < D)
-            p.part_o[(row0 + n) * D + r] = l > 0.f ? __uint_as_float(ov[n]) / l : 0.f;
-          if (r == 0) p.part_lse[row0 + n] = (m_run[n] + __log2f(l)) * 0.69314718055994531f;
+        if (k == 0 && tile_last >= 0) {
+          if (!finish(n_items - 1)) {
+            ok = false;
+            break;
+          }
         }
       }
+      ok = bar_red_and(1, 128, ok);  // (the warps go on, or leave, together)
+      if (!ok) break;
+#pragma unroll
+      for (int n = 0; n < kNQ; ++n) {
+        m_last[n] = m_run[n];
+        l_last[n] = lsum[n];
+      }
+      row_last = row0;
+      tile_last = tile - 1;
+      ++n_items;
     }
+    if (bar_red_and(1, 128, ok) && tile_last >= 0) finish(n_items - 1);
   }
 
   // ---- teardown: no MMA in flight, then free TMEM
@@ -483,12 +560,12 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
   if (blockIdx.x == 0 && p.behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int D>
+template <int D, int kNQ>
 int launch(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse, bool behind,
            cudaStream_t stream) {
   using C = OwnCfg<D>;
   static std::atomic<unsigned long long> attr{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_own_kernel<D>), C::kAlloc, attr))
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_own_kernel<D, kNQ>), C::kAlloc, attr))
     return SWA_ERR_CUDA;
   OwnParams p;
   std::memset(&p, 0, sizeof(p));
@@ -497,7 +574,7 @@ int launch(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part
   const uint64_t rows = (uint64_t)a.B * a.H;
   const uint64_t dims[4] = {(uint64_t)D, rows, 1, 1};
   const uint64_t strides[3] = {(uint64_t)D * 2, rows * D * 2, rows * D * 2};
-  const uint32_t box[4] = {64, kNQ, 1, 1};
+  const uint32_t box[4] = {64, kQRows, 1, 1};
   if (encode_tiled(&p.tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims,
                    strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return SWA_ERR_CUDA;
@@ -526,7 +603,7 @@ int launch(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part
   if (items > 0x7fffffffLL - 4096) return SWA_ERR_UNSUPPORTED;
   p.items = (int)items;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < 2 * pl.sms ? items : 2 * pl.sms));
+  cfg.gridDim = dim3((unsigned)(items < pl.sms ? items : pl.sms));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kAlloc;
   cfg.stream = stream;
@@ -535,15 +612,21 @@ int launch(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, swa_own_kernel<D>, p) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, swa_own_kernel<D, kNQ>, p) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_own(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
                bool behind, cudaStream_t stream) {
-  if (a.D == 128) return launch<128>(a, pl, part_o, part_lse, behind, stream);
-  if (a.D == 64) return launch<64>(a, pl, part_o, part_lse, behind, stream);
+  // (groups of up to four take the form that carries four values)
+  const bool four = a.H / a.Hkv <= 4;
+  if (a.D == 128)
+    return four ? launch<128, 4>(a, pl, part_o, part_lse, behind, stream)
+                : launch<128, 8>(a, pl, part_o, part_lse, behind, stream);
+  if (a.D == 64)
+    return four ? launch<64, 4>(a, pl, part_o, part_lse, behind, stream)
+                : launch<64, 8>(a, pl, part_o, part_lse, behind, stream);
   return SWA_ERR_UNSUPPORTED;
 }
 

@@ -129,7 +129,7 @@ SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int ma
   // sequences do not fill two CTAs per SM
   const long long tail = (max_tail < W ? max_tail : W) + (long long)kBlockRows - 1;
   long long own = (tail + 1023) / 1024;
-  const long long fill = (2 * sms + (long long)B * Hkv - 1) / ((long long)B * Hkv);
+  const long long fill = (sms + (long long)B * Hkv - 1) / ((long long)B * Hkv);
   const long long most = (tail + 255) / 256;
   if (own < fill) own = fill < most ? fill : most;
   pl.own_parts = (int)(own < 1 ? 1 : own);
