@@ -459,11 +459,16 @@ def _ready(dev, *tensors):
     return True
 
 
+# (of a CUDA tensor's device, so CUDA is initialised)
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _run(dev, stream, name, *args):
     """Calls the library's `name` with the stream appended, on device `dev`."""
     fn = getattr(_lib, name)
-    if dev == torch.cuda.current_device():
-        status = fn(*args, _stream(stream))
+    if dev == _device():
+        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _stream(stream))

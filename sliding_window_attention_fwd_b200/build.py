@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,7 +25,7 @@ def sources():
 
 def deps():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
-        glob.glob(os.path.join(INCLUDE, "*.h")))
+        glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def stale() -> bool:
@@ -39,10 +40,20 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str | None:
     if not srcs:
         return None
     if force or stale():
-        cmd = ["nvcc", *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", LIB, *srcs]
-        if verbose:
-            print(" ".join(cmd))
-        subprocess.check_call(cmd)
+        # every source in its own nvcc process, then the link
+        flags = [f for f in NVCC_FLAGS if f != "-shared"]
+        with tempfile.TemporaryDirectory() as tmp:
+            objs, procs = [], []
+            for src in srcs:
+                objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
+                cmd = ["nvcc", *flags, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", objs[-1]]
+                if verbose:
+                    print(" ".join(cmd))
+                procs.append((cmd, subprocess.Popen(cmd)))
+            failed = [cmd for cmd, proc in procs if proc.wait() != 0]
+            if failed:
+                raise subprocess.CalledProcessError(1, failed[0])
+            subprocess.check_call(["nvcc", *NVCC_FLAGS, "-o", LIB, *objs])
     return LIB
 
 

@@ -135,8 +135,8 @@ def lib(monkeypatch):
     monkeypatch.setattr(b, "_lib", rec)
     monkeypatch.setattr(b, "_placed", lambda ref, **kw: None)
     monkeypatch.setattr(b, "_token_rows", lambda x, n, dev: x.stride(0))
-    monkeypatch.setattr(b, "_stream", lambda s: "STREAM")
-    monkeypatch.setattr(b.torch.cuda, "current_device", lambda: -1)  # what CPU tensors say
+    monkeypatch.setattr(b, "_device", lambda: -1)  # what CPU tensors say
+    monkeypatch.setattr(b, "_raw_stream", lambda d: "STREAM")
     return rec
 
 
