@@ -152,59 +152,99 @@ __device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
 }
 
 // Shaped scores of 32 raw products of one thread (its row r against the
-// columns c0 .. c0 + 31): x = cap(scale qk) - slope |i - j| in log2 units, and
-// fac = 1 - tanh^2, the cap's derivative.  The bias is linear in the column
-// while the chunk lies on one side of every row of the warp (add0, step: of
-// the columns 2e, 2e + 1); on the diagonal it takes |i - j| per column.
-template <int SC>
-struct Shape {
-  float2 add0, step;
-  float base, nslope2;
-  bool diag, small;
-  __device__ __forceinline__ Shape(const CapCoefs& c, float nslope2_, const uint32_t (&sv)[32],
-                                   int r, int c0) {
-    add0 = step = make_float2(0.f, 0.f);
-    base = 0.f;
-    diag = false;
-    small = true;
-    nslope2 = nslope2_;
-    if (SC & 2) {
-      const int lo = r - (int)(threadIdx.x & 31) - c0;  // the warp's first row
-      base = (float)(r - c0);
-      diag = lo < 31 && lo + 31 > 0;
-      const float k1 = lo >= 31 ? -nslope2 : nslope2;
-      add0 = make_float2(-k1 * base, fmaf(-k1, base, k1));
-      step = make_float2(2.f * k1, 2.f * k1);
-    }
-    if (SC & 1) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
+// columns c0 .. c0 + 31): x = cap(scale qk) - slope |i - j| + nl in log2 units
+// (nl(e): minus the lse of the columns 2e and 2e + 1), and t, the cap's tanh.
+// The bias is linear in the column while the chunk lies on one side of every
+// row of the warp (add0, step: of the columns 2e and 2e + 1); on the diagonal
+// it takes |i - j| per column.
+template <int SC, class NegLse>
+__device__ __forceinline__ void shape_chunk(const CapCoefs& c, float scale_log2, float nslope2,
+                                            const uint32_t (&sv)[32], int r, int c0, NegLse nl,
+                                            float2 (&x)[16], float2 (&t)[16]) {
+  float2 add0 = make_float2(0.f, 0.f), step = add0;
+  float base = 0.f;
+  bool diag = false;
+  if (SC & 2) {
+    const int lo = r - (int)(threadIdx.x & 31) - c0;  // the warp's first row
+    base = (float)(r - c0);
+    diag = lo < 31 && lo + 31 > 0;
+    const float k1 = lo >= 31 ? -nslope2 : nslope2;
+    add0 = make_float2(-k1 * base, fmaf(-k1, base, k1));
+    step = make_float2(2.f * k1, 2.f * k1);
+  }
+  auto raw = [&](int e) {
+    return make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]));
+  };
+  if (SC & 1) {
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        t[e / 2 & 3] = max3f(t[e / 2 & 3], fabsf(__uint_as_float(sv[e])),
-                             fabsf(__uint_as_float(sv[e + 1])));
-      small = !__any_sync(0xffffffffu, max3f(t[0], t[1], fmaxf(t[2], t[3])) > c.small);
+    for (int e = 0; e < 16; ++e)
+      m[e & 3] = max3f(m[e & 3], fabsf(raw(e).x), fabsf(raw(e).y));
+    if (!__any_sync(0xffffffffu, max3f(m[0], m[1], fmaxf(m[2], m[3])) > c.small)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) t[e] = tanh_small(c, raw(e));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        t[e] = make_float2(tanh_any(c, raw(e).x), tanh_any(c, raw(e).y));
     }
   }
-  // Columns 2e and 2e + 1, nl being -lse.
-  template <bool kSmall>
-  __device__ __forceinline__ float2 pair(const CapCoefs& c, float scale_log2, float2 s, int e,
-                                         float2 nl, float2* fac) const {
-    if (SC & 2) {
-      if (diag)
-        nl = make_float2(fmaf(nslope2, fabsf(base - (float)(2 * e)), nl.x),
-                         fmaf(nslope2, fabsf(base - (float)(2 * e + 1)), nl.y));
-      else
-        nl = add2(nl, fma2(make_float2((float)e, (float)e), step, add0));
+  const float2 unit = (SC & 1) ? make_float2(c.out, c.out) : make_float2(scale_log2, scale_log2);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = fma2((SC & 1) ? t[e] : raw(e), unit, nl(e));
+  if (SC & 2) {
+    if (diag) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e].x = fmaf(nslope2, fabsf(base - (float)(2 * e)), x[e].x);
+        x[e].y = fmaf(nslope2, fabsf(base - (float)(2 * e + 1)), x[e].y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x[e] = add2(x[e], fma2(make_float2((float)e, (float)e), step, add0));
     }
+  }
+}
+
+// P = 2^x of 32 scores and, with a cap, its derivative's factor: pr = P (1 -
+// t^2); without one, pr = P.  Columns outside [lo, hi] (counted from 0; edge)
+// get 0, whatever their products were.  P goes to `each` pair by pair.  With a
+// cap the FMA pipe has enough to do and all exponentials go to MUFU, else half
+// of the inner tiles'.
+template <int SC, class Each>
+__device__ __forceinline__ void exp_chunk(bool edge, int lo, int hi, float2 (&x)[16],
+                                          float2 (&t)[16], float2 (&pr)[16], Each each) {
+  if (edge) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (2 * e < lo || 2 * e > hi) {
+        x[e].x = -INFINITY;
+        if (SC & 1) t[e].x = 0.f;
+      }
+      if (2 * e + 1 < lo || 2 * e + 1 > hi) {
+        x[e].y = -INFINITY;
+        if (SC & 1) t[e].y = 0.f;
+      }
+    }
+  }
+  auto out = [&](int e, float2 p) {
+    each(e, p);
     if (SC & 1) {
-      const float2 t =
-          kSmall ? tanh_small(c, s) : make_float2(tanh_any(c, s.x), tanh_any(c, s.y));
-      *fac = fma2(mul2(t, t), make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
-      return fma2(t, make_float2(c.out, c.out), nl);
+      const float2 f = fma2(mul2(t[e], t[e]), make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+      pr[e] = mul2(p, f);
+    } else {
+      pr[e] = p;
     }
-    return fma2(s, make_float2(scale_log2, scale_log2), nl);
+  };
+  if ((SC & 1) || edge) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) out(e, make_float2(ex2_approx(x[e].x), ex2_approx(x[e].y)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) out(e, exp2_pair(x[e], (e & 1) != 0));
   }
-};
+}
 
 // Zeros over the rows of a 128-row tile outside [z0, z1) (thread r: row r of
 // the tile at row0): padding may hold anything, and a product with P = 0 or
@@ -471,32 +511,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_wait_ld();
         const int n0 = t * kTileN + 32 * ch;
         if constexpr (kShaped) {
-          const Shape<SC> shp(p.cap, nslope2, sv, m_v, n0);
-          auto columns = [&](auto is_small) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 fac;
-              float2 xs = shp.template pair<decltype(is_small)::value>(
-                  p.cap, sl2, make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])),
-                  e, make_float2(-lse2, -lse2), &fac);
-              if (edge) {
-                const int j0 = n0 + 2 * e;
-                if (!(j0 >= klo && j0 <= khi)) xs.x = -INFINITY;
-                if (!(j0 + 1 >= klo && j0 + 1 <= khi)) xs.y = -INFINITY;
-              }
-              // (with a cap the FMA pipe has enough to do)
-              pr[i][e] = exp2_pair(xs, !(SC & 1) && (e & 1) != 0 && !edge);
-              if (SC & 1) {
-                if (edge) {  // a masked product may be NaN: its factor must not meet P = 0
-                  if (xs.x == -INFINITY) fac.x = 0.f;
-                  if (xs.y == -INFINITY) fac.y = 0.f;
-                }
-                pr[i][e] = mul2(pr[i][e], fac);
-              }
-            }
-          };
-          if (shp.small) columns(std::true_type());
-          else columns(std::false_type());
+          float2 x[16], t[16];
+          shape_chunk<SC>(p.cap, sl2, nslope2, sv, m_v, n0,
+                          [&](int) { return make_float2(-lse2, -lse2); }, x, t);
+          exp_chunk<SC>(edge, klo - n0, khi - n0, x, t, pr[i], [](int, float2) {});
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -846,37 +864,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const float4* l4 = reinterpret_cast<const float4*>(vl + 32 * ch);
         uint32_t pp[16];
         if constexpr (kShaped) {
-          const Shape<SC> shp(p.cap, nslope2, sv, j_v, i0);
-          auto columns = [&](auto is_small) {
-#pragma unroll
-            for (int e2 = 0; e2 < 8; ++e2) {
-              const float4 l = l4[e2];  // lse2 of this pair of pairs
-#pragma unroll
-              for (int h2 = 0; h2 < 2; ++h2) {
-                const int e = 2 * e2 + h2;
-                float2 fac;
-                float2 xs = shp.template pair<decltype(is_small)::value>(
-                    p.cap, sl2,
-                    make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), e,
-                    h2 ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y), &fac);
-                if (edge) {
-                  if (!(i0 + 2 * e >= qlo && i0 + 2 * e <= qhi)) xs.x = -INFINITY;
-                  if (!(i0 + 2 * e + 1 >= qlo && i0 + 2 * e + 1 <= qhi)) xs.y = -INFINITY;
-                }
-                pr[i][e] = exp2_pair(xs, !(SC & 1) && h2 != 0 && !edge);
-                pp[e] = pack_bf16x2(pr[i][e].x, pr[i][e].y);
-                if (SC & 1) {
-                  if (edge) {
-                    if (xs.x == -INFINITY) fac.x = 0.f;
-                    if (xs.y == -INFINITY) fac.y = 0.f;
-                  }
-                  pr[i][e] = mul2(pr[i][e], fac);
-                }
-              }
-            }
-          };
-          if (shp.small) columns(std::true_type());
-          else columns(std::false_type());
+          float2 x[16], t[16];
+          shape_chunk<SC>(p.cap, sl2, nslope2, sv, j_v, i0,
+                          [&](int e) {
+                            const float4 l = l4[e / 2];
+                            return e & 1 ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y);
+                          },
+                          x, t);
+          exp_chunk<SC>(edge, qlo - i0, qhi - i0, x, t, pr[i],
+                        [&](int e, float2 v) { pp[e] = pack_bf16x2(v.x, v.y); });
         } else {
 #pragma unroll
           for (int e2 = 0; e2 < 8; ++e2) {

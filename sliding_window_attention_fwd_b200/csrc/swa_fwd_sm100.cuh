@@ -1293,7 +1293,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 
     // split key walk: this CTA's part goes to the partials (fp32 O / l and
     // lse); an empty part contributes nothing (lse = -inf)
-    const bool split = shared || (qwin && p.nsplit > 1 && !pair);
+    const bool split = p.nsplit > (shared ? 0 : 1) && (shared || (qwin && !pair));
     const size_t prow = shared ? ((size_t)sp * p.B + sR / grp) * p.H + h
                                : (((size_t)sp * p.B + b) * p.H + h) * (size_t)Mq + m_row;
     if (split && ok && n_tiles == 0 && row_valid && !warp_idle) {
