@@ -374,6 +374,17 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
   const bool block_mode = p.bs > 1;
   const int map_idx = block_mode ? 0 : cl;
 
+  // Key tile of step it.  With a distance bias the nearest keys come first
+  // (the diagonal tile, those before it, then those behind): walked from far
+  // to near, a steep bias would raise the running maximum on every tile.
+  int near = tr.kv_end - 1;
+  if (docs && (SC & 2)) near = min(near, max(tr.kv_begin, qt));
+  auto kv_tile = [&](int it) -> int {
+    if (!(SC & 2)) return tr.kv_begin + it;
+    const int before = near - tr.kv_begin + 1;
+    return it < before ? near - it : tr.kv_begin + it;
+  };
+
   // virtual row -> TMA row coordinate of a 64-row box
   auto box_row = [&](int vrow) -> int {
     return block_mode ? (c + p.d * (vrow / kBlockRows)) * kBlockRows : vrow;
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     const int st = it % kStages;
     uint64_t* ful = kv ? &full_v[st] : &full_k[st];
     uint8_t* dst = smem + C::kRing + st * C::kStageBytes + kv * NSTREAM * C::kTile;
-    const int t = tr.kv_begin + it;
+    const int t = kv_tile(it);
     mbar_arrive_expect_tx(ful, NSTREAM * C::kTile);
     for (int hh = 0; hh < 2; ++hh) {
       int row;
@@ -848,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       q.diag = false;
       q.small = true;
       if (bias_on) {
-        const int n0 = (tr.kv_begin + it) * kTileN + hf * 64;
+        const int n0 = kv_tile(it) * kTileN + hf * 64;
         // rows of the warp relative to the half's first key (keys of a shared
         // prefix never lie behind a row that sees them)
         const int lo = shared ? 64 : m_v - lane - n0, hi = lo + 31;
@@ -872,26 +883,33 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       }
       return q;
     };
-    // Keys 2e and 2e + 1 of the half; kLinear: not on the diagonal.
-    auto shape_pair = [&](const HalfShape& q, int e, float2 s, auto is_small,
-                          auto is_linear) -> float2 {
-      float2 add = make_float2(q.add, q.add);
-      if (bias_on) {
-        if (decltype(is_linear)::value)
-          add = make_float2(fmaf(q.k1, (float)(2 * e), q.add), fmaf(q.k1, (float)(2 * e + 1), q.add));
-        else
-          add = make_float2(fmaf(nslope2, fabsf(q.base - (float)(2 * e)), q.add),
-                            fmaf(nslope2, fabsf(q.base - (float)(2 * e + 1)), q.add));
+    // Addends of the keys 2e and 2e + 1, for e in order: bias and -m_ref.  Off
+    // the diagonal they are stepped through, afresh every eight pairs, so
+    // that at most seven roundings add up.
+    auto next_addend = [&](const HalfShape& q, int e, auto is_linear, float2& add) {
+      if (!bias_on) {
+        add = make_float2(q.add, q.add);
+      } else if (!decltype(is_linear)::value) {
+        add = make_float2(fmaf(nslope2, fabsf(q.base - (float)(2 * e)), q.add),
+                          fmaf(nslope2, fabsf(q.base - (float)(2 * e + 1)), q.add));
+      } else if ((e & 7) == 0) {
+        add.x = fmaf(q.k1, (float)(2 * e), q.add);
+        add.y = fmaf(q.k1, (float)(2 * e + 1), q.add);
+      } else {
+        add = add2(add, make_float2(2.f * q.k1, 2.f * q.k1));
       }
+    };
+    auto shape_pair = [&](float2 s, float2 add, auto is_small) -> float2 {
       if (!cap_on) return fma2(s, make_float2(sl2, sl2), add);
       return decltype(is_small)::value ? cap_small(p.cap, s, add) : cap_any(p.cap, s, add);
     };
     auto shape_half = [&](const HalfShape& q, float (&sv)[64]) {
       auto run = [&](auto is_small, auto is_linear) {
+        float2 add;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 x =
-              shape_pair(q, e, make_float2(sv[2 * e], sv[2 * e + 1]), is_small, is_linear);
+          next_addend(q, e, is_linear, add);
+          const float2 x = shape_pair(make_float2(sv[2 * e], sv[2 * e + 1]), add, is_small);
           sv[2 * e] = x.x;
           sv[2 * e + 1] = x.y;
         }
@@ -909,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     auto clear_v_rows = [&](int it, int z0, int z1) -> bool {
       const int st = it % kStages;
       if (!mbar_wait(&full_v[st], (uint32_t)(it / kStages) & 1u, p.err, abort_flag)) return false;
-      const int j = (tr.kv_begin + it) * kTileN + r;
+      const int j = kv_tile(it) * kTileN + r;
       if (j < z0 || j >= z1) {
         uint8_t* vt = smem + C::kRing + st * C::kStageBytes + NSTREAM * C::kTile;
 #pragma unroll 1
@@ -927,7 +945,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       uint64_t keep = ~0ull;
       if (!glob || it < n_band) {
         if (edge) {
-          const int n0 = (tr.kv_begin + it) * kTileN + hf * 64;
+          const int n0 = kv_tile(it) * kTileN + hf * 64;
           const int lo = max(klo - n0, 0);
           const int hi = min(min(khi, Mv - 1) - n0, 63);  // inclusive
           keep = hi < lo ? 0ull : ((~0ull >> (63 - hi)) & (~0ull << lo));
@@ -1005,6 +1023,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     // (2.6e-6), so that lse keeps fp32 accuracy.
     auto exp_shaped = [&](int pcol, float (&sv)[64], float2 (&ls)[4], const HalfShape& q,
                           auto raw) {
+      float2 add;
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj) {
         uint32_t pk[16];
@@ -1013,7 +1032,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
           const int c = jj * 16 + e;
           float2 xa = make_float2(sv[2 * c], sv[2 * c + 1]);
           if (decltype(raw)::value) {
-            xa = shape_pair(q, c, xa, std::true_type(), std::true_type());
+            next_addend(q, c, std::true_type(), add);
+            xa = shape_pair(xa, add, std::true_type());
             sv[2 * c] = xa.x;
             sv[2 * c + 1] = xa.y;
           }
@@ -1082,7 +1102,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     for (int it = 0; ok && !warp_idle && it < n_tiles; ++it) {
       const int e = it & 1;  // early key half; P of the tile lives in its columns
       const uint32_t ph = (uint32_t)it & 1u;
-      const int t_kv = tr.kv_begin + it;
+      const int t_kv = kv_tile(it);
       const bool edge = ((!glob || it < n_band) && !(t_kv >= int_lo && t_kv <= int_hi)) ||
                         (inplace && t_kv * kTileN < gap_hi && t_kv * kTileN + kTileN > gap_lo);
 

@@ -167,6 +167,12 @@ __device__ __forceinline__ Item item_of(const OwnParams& p, int i) {
   return t;
 }
 
+// First key of tile k: from the last tile backwards, so that with a distance
+// bias the nearest keys come first and the running maximum holds.
+__device__ __forceinline__ int tile_key(const Item& t, int k) {
+  return t.s0 + (t.ntiles - 1 - k) * kTK;
+}
+
 template <int D, int kNQ>
 __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
     swa_own_kernel(const __grid_constant__ OwnParams p) {
@@ -245,8 +251,8 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
         // pages of tile k's two 64-row boxes (-1: read as zeros), looked up
         // one tile ahead
         auto page_at = [&](int k, int hh) -> int {
-          const int idx0 = t.s0 + k * kTK + hh * 64;
-          return idx0 < t.s1 ? __ldg(table + (t.a64 + idx0) / p.page_size) : -1;
+          const int idx0 = tile_key(t, k) + hh * 64;
+          return k < t.ntiles && idx0 < t.s1 ? __ldg(table + (t.a64 + idx0) / p.page_size) : -1;
         };
         int ahead[2] = {page_at(0, 0), page_at(0, 1)};
         for (int k = 0; ok && k < t.ntiles; ++k) {
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
           for (int hh = 0; hh < 2; ++hh) {
             row[hh] = ahead[hh] >= 0 && ahead[hh] < p.num_pages
                           ? ahead[hh] * p.page_size +
-                                (int)((t.a64 + t.s0 + k * kTK + hh * 64) % p.page_size)
+                                (int)((t.a64 + tile_key(t, k) + hh * 64) % p.page_size)
                           : -64;
             ahead[hh] = page_at(k + 1, hh);
           }
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
                          : 0.f;
       }
       for (int k = 0; k < t.ntiles; ++k, ++tile) {
-        const int k0 = t.s0 + k * kTK;  // the tile's first key
+        const int k0 = tile_key(t, k);  // the tile's first key
         const int idx = k0 + r;
         const bool valid = idx < t.s1 && idx >= t.lo;
         bool w_ok = true;
