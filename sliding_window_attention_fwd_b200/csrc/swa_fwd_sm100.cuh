@@ -1019,8 +1019,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
     // The same for shaped scores, whose maximum is already taken off.  raw: sv
     // holds the raw products still (linear bias, cap in its usual range) and
     // is shaped on the way, so that the FMA pipe works on some keys while MUFU
-    // works on others.  The pairs on the FMA pipe take the finer polynomial
-    // (2.6e-6), so that lse keeps fp32 accuracy.
+    // works on others.  (All exponentials go to MUFU: here the issue slots are
+    // scarcer, and 1/8 on the FMA pipe measured no faster.)
     auto exp_shaped = [&](int pcol, float (&sv)[64], float2 (&ls)[4], const HalfShape& q,
                           auto raw) {
       float2 add;
@@ -1037,13 +1037,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
             sv[2 * c] = xa.x;
             sv[2 * c + 1] = xa.y;
           }
-          float2 pr;
-          if (D != 64 && (e & 7) == 7) {
-            pr = exp2_poly2_fine(xa);
-          } else {
-            pr.x = ex2_approx(xa.x);
-            pr.y = ex2_approx(xa.y);
-          }
+          const float2 pr = make_float2(ex2_approx(xa.x), ex2_approx(xa.y));
           ls[e & 3] = add2(ls[e & 3], pr);
           pk[e] = pack_bf16x2(pr.x, pr.y);
         }
@@ -1435,8 +1429,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
       tc_fence_after();
       // (l == 0: a part of a split walk with none of the row's keys, whose
       // lse is -inf and which the merge skips, or a padding row: zeros)
-      // (the polynomial exponential leaves 2^-125 of a masked score, so l of a
-      // row without keys need not be 0; its maximum tells)
+      // (a row without keys: its maximum never rose)
       const bool none = scored && m_used == -INFINITY;
       const float inv = l > 0.f && !none ? 1.f / l : 0.f;
       const size_t orow_i = qwin ? (size_t)b * Mq + m_row : (size_t)b * p.N + i_phys;

@@ -423,25 +423,6 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
                      __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
 
-// The same with a degree-4 polynomial (max relative error 2.6e-6, one more
-// FMA a pair), where the sum of the results is kept to fp32 accuracy.
-__device__ __forceinline__ float2 exp2_poly2_fine(float2 x) {
-  constexpr float kC0 = 0.99999925854f, kC1 = 0.69312180739f, kC2 = 0.24024745f,
-                  kC3 = 0.05591786f, kC4 = 0.0095701f;
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
-  const float2 t = add2(x, make_float2(kMagic, kMagic));
-  const float2 n = add2(t, make_float2(-kMagic, -kMagic));
-  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
-  float2 q = fma2(make_float2(kC4, kC4), f, make_float2(kC3, kC3));
-  q = fma2(q, f, make_float2(kC2, kC2));
-  q = fma2(q, f, make_float2(kC1, kC1));
-  q = fma2(q, f, make_float2(kC0, kC0));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
-}
-
 // Packs two floats to bf16x2 (round to nearest even): lo -> bits [0,16).
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
