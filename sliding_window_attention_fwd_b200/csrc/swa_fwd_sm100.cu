@@ -10,7 +10,7 @@ namespace {
 // form (paired parts); asked once per form.
 template <int D, int NSLOT, int NSTREAM>
 bool pair_clusters_fit() {
-  using C = Cfg<D, NSLOT, NSTREAM>;
+  using C = Cfg<D, NSLOT, NSTREAM, 1>;
   static std::atomic<int> known{0};  // 0 not asked, 1 yes, -1 no
   int k = known.load(std::memory_order_acquire);
   if (k == 0) {
@@ -39,7 +39,7 @@ template <int D, int NSLOT, int NSTREAM>
 int launch_impl(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H,
                 int Hkv, int N, int L, int R, int d, int bs, const int32_t* G, int ng,
                 float scale, cudaStream_t stream, const QueryWindow* qw, int qt_lo, int qt_hi) {
-  using C = Cfg<D, NSLOT, NSTREAM>;
+  using C = Cfg<D, NSLOT, NSTREAM, 0>;  // (the same for kinds 0 to 2)
   static std::atomic<unsigned long long> attr_kind[3] = {{0}, {0}, {0}};
   const int kind = qw ? 1 : (ng > 0 ? 2 : 0);
   const void* kfn[3] = {reinterpret_cast<const void*>(swa_fwd_sm100_kernel<D, NSLOT, NSTREAM, 0>),

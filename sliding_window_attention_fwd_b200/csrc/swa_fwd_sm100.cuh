@@ -152,7 +152,7 @@ struct FwdParams {
   int page_size, num_pages, keep;
 };
 
-template <int D, int NSLOT, int NSTREAM>
+template <int D, int NSLOT, int NSTREAM, int KIND>
 struct Cfg {
   static constexpr int kTile = D / 64 * kChunkBytes;        // 128 rows x D bf16
   static constexpr int kStageBytes = 2 * NSTREAM * kTile;   // K and V of every stream
@@ -160,14 +160,14 @@ struct Cfg {
   // one head at D = 64 is small enough for two CTAs per SM (shared memory,
   // TMEM and, with the register split below, registers), so one CTA's fill
   // and drain overlap the other's tiles
-  static constexpr int kMinBlocks = (NSLOT == 1 && D == 64) ? 2 : 1;
+  static constexpr int kMinBlocks = (NSLOT == 1 && (D == 64 || KIND == 3)) ? 2 : 1;
   static constexpr int kBudget = kMinBlocks == 2 ? 96 * 1024 : 224 * 1024;
   // TMEM: S/P of slot s at [128 s, 128 s + 128), O of slot s at kOcol + D s
   static constexpr uint32_t kOcol = 128u * NSLOT;
   static constexpr uint32_t kTmemCols = kOcol + NSLOT * D <= 256 ? 256u : 512u;
   static constexpr int kFit = (kBudget - kQBytes) / kStageBytes;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static_assert(kStages >= 2, "K/V ring needs two stages");
+  static_assert(kStages >= 1, "K/V ring");
   static constexpr int kThreads = 128 * (1 + NSLOT);
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + kQBytes;
@@ -192,10 +192,10 @@ struct Cfg {
 // band with shaped scores and documents; 4 the shared prefix of a decode.
 // SC (kinds 3 and 4): 1 a tanh cap, 2 a distance bias, 3 both.
 template <int D, int NSLOT, int NSTREAM, int KIND, int SC = 0>
-__global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
-                                  Cfg<D, NSLOT, NSTREAM>::kMinBlocks)
+__global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
+                                  Cfg<D, NSLOT, NSTREAM, KIND>::kMinBlocks)
     swa_fwd_sm100_kernel(const __grid_constant__ FwdParams p) {
-  using C = Cfg<D, NSLOT, NSTREAM>;
+  using C = Cfg<D, NSLOT, NSTREAM, KIND>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1530,7 +1530,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM>::kThreads,
 // checked once per kernel form.
 template <int D, int NSLOT, int NSTREAM, int KIND, int SC>
 bool fwd_regs_fit() {
-  using C = Cfg<D, NSLOT, NSTREAM>;
+  using C = Cfg<D, NSLOT, NSTREAM, KIND>;
   if (!(NSLOT == 2 || C::kMinBlocks == 2)) return true;
   const long need = NSLOT == 2 ? 128L * 56 + 256L * 208 : 128L * 56 + 128L * 200;
   static std::atomic<int> known{0};

@@ -21,16 +21,6 @@
 namespace swa {
 namespace {
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return 148;
-  }
-  return n;
-}
-
 // One warp per row (sequence, head): the parts' weights e^(lse_i - lse), 32 at
 // a time, one per lane, then the weighted sum of the parts, eight loads in
 // flight per lane.
@@ -110,6 +100,23 @@ int merge(const float* part_o, const float* part_lse, void* out, float* lse, int
 }
 
 }  // namespace
+
+int sm_count() {
+  constexpr int kMax = 64;
+  static std::atomic<int> known[kMax];  // by device, 0: not asked
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < kMax && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < kMax) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int max_tail) {
   SharedPlan pl;

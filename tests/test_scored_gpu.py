@@ -113,6 +113,16 @@ def test_documents(swa, name, D, prefix):
     run(swa, 1, 520, 2, 2, D, -1, 0, 0.0, True, cu=cu, pre=pre if prefix else None)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_two_heads_per_cta(swa, D, cap, bias):
+    """Enough work to fill the SMs with two heads per CTA."""
+    cu = [[0, 100, 101, 600, 700], [30, 260, 260, 500, 650]]
+    pre = [[40, 5, 300, 0], [10, 0, 100, 1000]]
+    run(swa, 2, 705, 32, 8, D, 300, 0, cap, bias, cu=cu, pre=pre)
+    run(swa, 1, 705, 64, 16, D, 130, 90, cap, bias)
+
+
 def test_batch_of_different_documents(swa):
     cu = [[0, 100, 300], [10, 10, 290], [0, 0, 0]]
     pre = [[0, 40], [7, 1000], [-3, 5]]
