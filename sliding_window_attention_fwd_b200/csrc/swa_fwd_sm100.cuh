@@ -160,7 +160,7 @@ struct Cfg {
   // one head at D = 64 is small enough for two CTAs per SM (shared memory,
   // TMEM and, with the register split below, registers), so one CTA's fill
   // and drain overlap the other's tiles
-  static constexpr int kMinBlocks = (NSLOT == 1 && (D == 64 || KIND == 3)) ? 2 : 1;
+  static constexpr int kMinBlocks = (NSLOT == 1 && (D == 64 || KIND >= 3)) ? 2 : 1;
   static constexpr int kBudget = kMinBlocks == 2 ? 96 * 1024 : 224 * 1024;
   // TMEM: S/P of slot s at [128 s, 128 s + 128), O of slot s at kOcol + D s
   static constexpr uint32_t kOcol = 128u * NSLOT;

@@ -128,13 +128,14 @@ struct SharedArgs {
 // (part_keys keys each, the last part taking what is left).
 struct SharedPlan {
   int prefix_parts, own_parts, part_keys, sms;
+  bool two;  // two query tiles per CTA of the prefix
   size_t bytes;  // workspace: O / l and lse of every part
 };
 SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int max_tail);
 int launch_decode_shared(SharedArgs a, const SharedPlan& pl, void* workspace,
                          cudaStream_t stream);
 // The prefix's share: parts 0 .. nsplit - 1 of the partial results.
-int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
+int launch_prefix(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
                   cudaStream_t stream);
 // The own keys' share; behind: right behind launch_prefix on the stream.
 int launch_own(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,

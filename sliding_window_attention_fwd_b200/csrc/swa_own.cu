@@ -64,7 +64,7 @@ struct OwnParams {
 template <int D>
 struct OwnCfg {
   static constexpr int kTile = kTK * D * 2;            // one K or V tile
-  static constexpr int kSlots = D == 128 ? 6 : 11;     // ring of tiles
+  static constexpr int kSlots = D == 128 ? 3 : 5;     // ring of tiles
   static constexpr int kPad = D == 128 ? 0 : kSlice;
   static constexpr int kQBytes = kQRows * D * 2;       // 8 rows, 1 KB per 64 columns
   static constexpr int kPBytes = kQRows * kTK * 2;     // P^T: 8 rows x 128 keys
@@ -80,7 +80,7 @@ struct OwnCfg {
   static constexpr int kAlloc = kMisc + 16 + 1024;     // slack for 1024-byte alignment
   static constexpr int kThreads = 192;
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "operand alignment");
-  static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(2 * (kAlloc + 1024) <= 233472, "two CTAs per SM");
 };
 
 // S^T buffers at columns 0 and 16, O^T at 32 and 48
@@ -174,7 +174,7 @@ __device__ __forceinline__ int tile_key(const Item& t, int k) {
 }
 
 template <int D, int kNQ>
-__global__ void __launch_bounds__(OwnCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
     swa_own_kernel(const __grid_constant__ OwnParams p) {
   using C = OwnCfg<D>;
   constexpr int S_ = C::kSlots;
@@ -609,7 +609,7 @@ int launch(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part
   if (items > 0x7fffffffLL - 4096) return SWA_ERR_UNSUPPORTED;
   p.items = (int)items;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < pl.sms ? items : pl.sms));
+  cfg.gridDim = dim3((unsigned)(items < 2 * pl.sms ? items : 2 * pl.sms));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kAlloc;
   cfg.stream = stream;

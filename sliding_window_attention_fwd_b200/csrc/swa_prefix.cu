@@ -53,8 +53,9 @@ int launch(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
 
 }  // namespace
 
-int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
+int launch_prefix(const SharedArgs& a, const SharedPlan& pl, float* part_o, float* part_lse,
                   cudaStream_t stream) {
+  const int nsplit = pl.prefix_parts;
   ScoreArgs sc;
   sc.softcap = a.softcap;
   sc.slopes = a.slopes;
@@ -69,14 +70,13 @@ int launch_prefix(const SharedArgs& a, int nsplit, float* part_o, float* part_ls
   };
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
-  const bool two = (long long)a.B * (a.H / a.Hkv) > kTileM;  // more than one query tile
   if (a.D == 128) {
     using D128 = std::integral_constant<int, 128>;
-    return two ? go(D128(), I2()) : go(D128(), I1());
+    return pl.two ? go(D128(), I2()) : go(D128(), I1());
   }
   if (a.D == 64) {
     using D64 = std::integral_constant<int, 64>;
-    return two ? go(D64(), I2()) : go(D64(), I1());
+    return pl.two ? go(D64(), I2()) : go(D64(), I1());
   }
   return SWA_ERR_UNSUPPORTED;
 }

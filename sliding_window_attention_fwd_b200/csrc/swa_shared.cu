@@ -123,20 +123,23 @@ SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int ma
   pl.sms = sm_count();
   const long long sms = pl.sms;
   // prefix: query tiles x kv heads, each walk split until the SMs are full
-  // (one CTA of two query tiles per SM; of one tile at D = 64, two)
   const long long rows = (long long)B * (H / Hkv);
-  const bool two = rows > kTileM;
-  const long long per_item = two ? 2 * kTileM : kTileM;
-  const long long items = (rows + per_item - 1) / per_item * Hkv;
   const long long tiles = ((long long)n_prefix + kTileN - 1) / kTileN;
-  long long parts = sms * (!two && D == 64 ? 2 : 1) / items;
-  parts = parts < 1 ? 1 : parts;
-  pl.prefix_parts = (int)(parts < tiles ? parts : tiles);
+  auto parts_of = [&](int per_item, int per_sm) -> long long {
+    const long long items = (rows + per_item - 1) / per_item * Hkv;
+    const long long parts = sms * per_sm / items;
+    return parts < 1 ? 1 : (parts < tiles ? parts : tiles);
+  };
+  // (measured with 256 rows of 128 against one tile per CTA, two CTAs per SM:
+  // 44.8 and 46.6 us for 64 sequences behind 8192 tokens, 154 and 178 us for
+  // 128 behind 32741)
+  pl.two = rows > kTileM;
+  pl.prefix_parts = (int)(pl.two ? parts_of(2 * kTileM, 1) : parts_of(kTileM, 2));
   // own keys: at most about 1024 per part; fewer, down to 256, while the
   // sequences do not fill two CTAs per SM
   const long long tail = (max_tail < W ? max_tail : W) + (long long)kBlockRows - 1;
   long long own = (tail + 1023) / 1024;
-  const long long fill = (sms + (long long)B * Hkv - 1) / ((long long)B * Hkv);
+  const long long fill = (2 * sms + (long long)B * Hkv - 1) / ((long long)B * Hkv);
   const long long most = (tail + 255) / 256;
   if (own < fill) own = fill < most ? fill : most;
   pl.own_parts = (int)(own < 1 ? 1 : own);
@@ -160,7 +163,7 @@ int launch_decode_shared(SharedArgs a, const SharedPlan& pl, void* workspace,
   a.tmK = &tm[0];
   a.tmV = &tm[1];
   if (pl.prefix_parts > 0) {
-    const int st = launch_prefix(a, pl.prefix_parts, part_o, part_lse, stream);
+    const int st = launch_prefix(a, pl, part_o, part_lse, stream);
     if (st != SWA_OK) return st;
   }
   const int st = launch_own(a, pl, part_o + (size_t)pl.prefix_parts * rows * a.D,
