@@ -66,6 +66,9 @@ namespace {
 constexpr int kMaxClasses = 8;   // residue classes per launch (tensor maps in params)
 constexpr int kChunkBytes = kTileM * 128;  // one 64-column slice of a 128-row tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// of the shaped forms, whose rows begin against 0 (P <= 2^32 is as good in bf16
+// and fp32)
+constexpr float kRescaleShaped = 32.0f;
 struct FwdParams {
   CUtensorMap tmQ[kMaxClasses];
   CUtensorMap tmK[kMaxClasses];
@@ -251,6 +254,22 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   x /= shared ? 1 : p.B;
   int cl = 0, qt = 0, gq0 = 0, gcnt = 0;
   const int sr0 = shared ? x * NSLOT * kTileM : 0;  // first query row of this item
+  // the item's query rows (zeros past the last), all loads in flight at once
+  // while the key range is found
+  constexpr int kC16 = D / 8;  // 16-byte chunks per row; also chunks per thread
+  uint4 q_val[shared ? kC16 : 1];
+  if (shared && threadIdx.x >= 128) {
+    const int grp_ = p.H / p.Hkv;
+#pragma unroll
+    for (int u = 0; u < kC16; ++u) {
+      const int idx = (int)threadIdx.x - 128 + u * 128 * NSLOT;
+      const int R = sr0 + idx / kC16, c16 = idx % kC16;
+      q_val[shared ? u : 0] = make_uint4(0u, 0u, 0u, 0u);
+      if (R < p.B * grp_)
+        q_val[shared ? u : 0] = __ldg(reinterpret_cast<const uint4*>(
+            p.q_raw + ((size_t)(R / grp_) * p.H + (size_t)g_kv * grp_ + R % grp_) * D + c16 * 8));
+    }
+  }
   if (shared) {
   } else if (gitem) {
     gq0 = x * kTileM;  // first global row of this tile
@@ -501,19 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     tmem_relinquish();
   }
   if (shared && n_tiles > 0 && threadIdx.x >= 128) {
-    // gather the item's query rows (zeros past the last) into the swizzled
-    // layout of a TMA box
-    constexpr int kC16 = D / 8;  // 16-byte chunks per row; also rounds of the loop below
-    uint4 val[kC16];             // every load in flight at once
-#pragma unroll
-    for (int u = 0; u < kC16; ++u) {
-      const int idx = (int)threadIdx.x - 128 + u * 128 * NSLOT;
-      const int R = sr0 + idx / kC16, c16 = idx % kC16;
-      val[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (R < p.B * grp)
-        val[u] = __ldg(reinterpret_cast<const uint4*>(
-            p.q_raw + ((size_t)(R / grp) * p.H + (size_t)g_kv * grp + R % grp) * D + c16 * 8));
-    }
+    // the query rows in the swizzled layout of a TMA box
 #pragma unroll
     for (int u = 0; u < kC16; ++u) {
       const int idx = (int)threadIdx.x - 128 + u * 128 * NSLOT;
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       const int rr = row % kTileM;
       uint8_t* d8 = smem + C::kQ + (row / kTileM) * C::kTile + (c16 / 8) * kChunkBytes + rr * 128 +
                     (((c16 % 8) ^ (rr % 8)) * 16);
-      *reinterpret_cast<uint4*>(d8) = val[u];
+      *reinterpret_cast<uint4*>(d8) = q_val[shared ? u : 0];
     }
     fence_proxy_async_smem();
   }
@@ -1138,12 +1145,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           }
           const float m_ref = m_used == -INFINITY ? 0.f : m_used;
           const HalfShape q = half_shape(it, hf, sv, m_ref);
-          const bool first = __any_sync(0xffffffffu, m_used == -INFINITY);
           float2 lh[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
           // the usual half, with no key to mask: P is formed while the half's
-          // maximum is found; otherwise the maximum comes first
-          const bool usual = !first && !q.diag && q.small && !__any_sync(0xffffffffu, edge);
+          // maximum is found (a row's first against 0, which holds for any
+          // maximum in [-20, 64]); otherwise the maximum comes first
+          const bool usual = !q.diag && q.small && !__any_sync(0xffffffffu, edge);
           if (usual) {
             exp_shaped(pcol, sv, lh, q, std::true_type());
           } else {
@@ -1154,9 +1161,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           tmax = fmaxf(tmax, m_ref + hmax);
           const bool adopt = m_used == -INFINITY;
           const bool jump = !adopt && hmax > 64.f;
-          if (adopt) m_used = hmax;
-          const bool any_jump = __any_sync(0xffffffffu, jump);
-          if (any_jump) {
+          const bool holds = usual && hmax <= 64.f && hmax >= -20.f;
+          if (adopt) m_used = holds ? 0.f : hmax;
+          const bool redo = __any_sync(0xffffffffu, jump || (adopt && !holds)) || !usual;
+          if (__any_sync(0xffffffffu, jump)) {
             const float m_old = m_used;
             if (late) {
               // O must hold the early half's PV before it is scaled
@@ -1166,16 +1174,15 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
             if (!rescale_o(it, jump, m_ref + hmax)) { ok = false; break; }
             const float f = jump ? ex2_approx(m_old - m_used) : 1.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              ls[j] = make_float2(ls[j].x * f, ls[j].y * f);
-              lh[j] = make_float2(0.f, 0.f);
-            }
-            tmem_wait_st();
+            for (int j = 0; j < 4; ++j) ls[j] = make_float2(ls[j].x * f, ls[j].y * f);
           }
-          if (!usual || any_jump) {
+          if (redo) {
             const float d = m_used == -INFINITY ? 0.f : m_ref - m_used;
 #pragma unroll
             for (int j = 0; j < 64; ++j) sv[j] += d;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lh[j] = make_float2(0.f, 0.f);
+            tmem_wait_st();
             exp_shaped(pcol, sv, lh, q, std::false_type());
           }
 #pragma unroll
@@ -1187,7 +1194,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
         if (!ok) break;
         const float2 a2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
         l += a2.x + a2.y;
-        if (tmax > m_used + kRescaleThreshold) m_pend = tmax;
+        if (tmax > m_used + kRescaleShaped) m_pend = tmax;
         mbar_arrive(&p_full[slot]);
         continue;
       }
