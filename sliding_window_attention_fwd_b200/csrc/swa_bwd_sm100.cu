@@ -297,19 +297,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int g_kv = h / p.grp;
   const Geometry geo = make_geometry(p.N, p.L, p.R, p.d, p.bs);
   const int Mv = p.Mv[cl];
-  TileRange tr = tile_range(geo, Mv, qt);
-  DocTiles dt{};
-  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
-                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
-                   p.N, p.L, p.R};
-  if (kShaped) {
-    dt = doc_tiles<false>(dm, qt * kTileM, min(qt * kTileM + kTileM, Mv) - 1);
-    tr.kv_begin = dt.begin;
-    tr.kv_end = dt.end;
-  }
-  const int n_tiles = tr.kv_end - tr.kv_begin;
   const int map_idx = p.bs > 1 ? 0 : cl;
-
+  auto load_q = [&]() {
+    mbar_arrive_expect_tx(full_q, 2 * C::kTile);
+    load_tile<D>(smem, &p.tmQ[map_idx], full_q, p, c, h, qt * kTileM, b);
+    load_tile<D>(smem + C::kTile, &p.tmDO[map_idx], full_q, p, c, h, qt * kTileM, b);
+  };
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     mbar_init(full_q, 1);
@@ -325,7 +318,60 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_init(ds_full, 128 * kGroupsB);
     mbar_init(done, 1);
     fence_mbar_init();
+    prefetch_tensormap(&p.tmQ[map_idx]);
+    prefetch_tensormap(&p.tmDO[map_idx]);
+    prefetch_tensormap(&p.tmK[map_idx]);
+    prefetch_tensormap(&p.tmV[map_idx]);
+    if (kShaped) load_q();  // on their way while the row's documents are looked up
   }
+  // Delta_i = dO_i . out_i, the rows read whole by 16 (D = 128) or 8 lanes each,
+  // also before the documents are known (the dot products of padding rows are
+  // dropped below).  A thread per row, as the band's form has it, spends 5 of a
+  // short walk's 20 us here.
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per warp load
+  constexpr int kIters = kTileM / (4 * kGroupsB * kRows);
+  uint4 w_do[kShaped ? kIters : 1], w_o[kShaped ? kIters : 1];
+  if (kShaped && warp >= 4) {
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+      const int m = qt * kTileM + ((warp - 4) * kIters + i) * kRows + lane / kLanes;
+      w_do[kShaped ? i : 0] = w_o[kShaped ? i : 0] = make_uint4(0u, 0u, 0u, 0u);
+      if (m < p.N) {
+        const size_t at = (((size_t)b * p.N + m) * p.H + h) * D / 8 + lane % kLanes;
+        w_do[kShaped ? i : 0] = __ldg(reinterpret_cast<const uint4*>(p.dout) + at);
+        w_o[kShaped ? i : 0] = __ldg(reinterpret_cast<const uint4*>(p.out) + at);
+      }
+    }
+  }
+  TileRange tr = tile_range(geo, Mv, qt);
+  DocTiles dt{};
+  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  if (kShaped) {
+    dt = doc_tiles<false>(dm, qt * kTileM, min(qt * kTileM + kTileM, Mv) - 1);
+    tr.kv_begin = dt.begin;
+    tr.kv_end = dt.end;
+  }
+  const int n_tiles = tr.kv_end - tr.kv_begin;
+  if (kShaped && warp >= 4) {
+    float* part = reinterpret_cast<float*>(smem + C::kVec);
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+      const uint4 wa = w_do[kShaped ? i : 0], wo = w_o[kShaped ? i : 0];
+      const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xo[4] = {wo.x, wo.y, wo.z, wo.w};
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc = fmaf(__uint_as_float(xa[e] << 16), __uint_as_float(xo[e] << 16), acc);
+        acc = fmaf(__uint_as_float(xa[e] & 0xFFFF0000u), __uint_as_float(xo[e] & 0xFFFF0000u), acc);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (lane % kLanes == 0) part[((warp - 4) * kIters + i) * kRows + lane / kLanes] = acc;
+    }
+  }
+
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
@@ -340,14 +386,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 
   if (warp == 0) {
     // ============================== producer ==============================
-    if (lane == 0 && (!kShaped || n_tiles > 0)) {
-      prefetch_tensormap(&p.tmQ[map_idx]);
-      prefetch_tensormap(&p.tmDO[map_idx]);
-      prefetch_tensormap(&p.tmK[map_idx]);
-      prefetch_tensormap(&p.tmV[map_idx]);
-      mbar_arrive_expect_tx(full_q, 2 * C::kTile);
-      load_tile<D>(smem, &p.tmQ[map_idx], full_q, p, c, h, qt * kTileM, b);
-      load_tile<D>(smem + C::kTile, &p.tmDO[map_idx], full_q, p, c, h, qt * kTileM, b);
+    if (lane == 0) {
+      if (!kShaped) load_q();
       int last_k = -1, last_v = -1;
       for (int it = 0; it < n_tiles; ++it) {
         const int st = it % S_;
@@ -363,7 +403,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         load_tile<D>(kb + C::kTile, &p.tmV[map_idx], &full_v[st], p, c, g_kv, t * kTileN, b);
         last_v = it;
       }
-      if (*abort_flag) {  // leave no copy writing shared memory behind
+      // leave no copy writing shared memory behind
+      if (kShaped && n_tiles == 0) drain_copies(full_q, 1, 0, 0);
+      if (*abort_flag) {
         drain_copies(full_q, 1, 0, 0);
         drain_copies(full_k, S_, 0, last_k);
         drain_copies(full_v, S_, 0, last_v);
@@ -456,10 +498,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (SC & 2) nslope2 = -__ldg(p.slopes + h) * kLog2e;
     }
     // Delta_i = dO_i . out_i (each group sums a quarter of the row, the
-    // parts meet in shared memory) and lse in log2 units; rows past the
-    // class end get P = 0
+    // parts meet in shared memory; shaped: computed above) and lse in log2
+    // units; rows past the class end get P = 0
     float delta = 0.f, lse2 = INFINITY;
-    {
+    if (kShaped) {
+      const float d = reinterpret_cast<const float*>(smem + C::kVec)[r];
+      if (row_valid) {
+        const size_t li = ((size_t)b * p.H + h) * p.N + m_v;
+        if (real_row) {
+          lse2 = __ldg(p.lse + li) * kLog2e;
+          delta = d;
+        }
+        if (cg == 0) p.delta[li] = delta;
+      }
+    } else {
       float* part = reinterpret_cast<float*>(smem + C::kVec);  // [group][128]
       float acc0 = 0.f, acc1 = 0.f;
       if (real_row) {
@@ -657,20 +709,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int c = p.class0 + cl;
   const Geometry geo = make_geometry(p.N, p.L, p.R, p.d, p.bs);
   const int Mv = p.Mv[cl];
-  TileRange qr = qtile_range_keys(geo, Mv, kt * kTileN);
-  DocTiles dt{};
-  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
-                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
-                   p.N, p.L, p.R};
-  if (kShaped) {
-    dt = doc_tiles<true>(dm, kt * kTileN, min(kt * kTileN + kTileN, Mv) - 1);
-    qr.kv_begin = dt.begin;
-    qr.kv_end = dt.end;
-  }
-  const int grp = p.grp;
-  const int n_steps = (qr.kv_end - qr.kv_begin) * grp;  // (query tile, head of the group)
   const int map_idx = p.bs > 1 ? 0 : cl;
-
+  auto load_kv = [&]() {
+    mbar_arrive_expect_tx(full_kv, 2 * C::kTile);
+    load_tile<D>(smem, &p.tmK[map_idx], full_kv, p, c, g_kv, kt * kTileN, b);
+    load_tile<D>(smem + C::kTile, &p.tmV[map_idx], full_kv, p, c, g_kv, kt * kTileN, b);
+  };
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     mbar_init(full_kv, 1);
@@ -684,7 +728,25 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_init(done, 1);
     mbar_init(p_full, 128 * kGroupsB);
     fence_mbar_init();
+    prefetch_tensormap(&p.tmQ[map_idx]);
+    prefetch_tensormap(&p.tmDO[map_idx]);
+    prefetch_tensormap(&p.tmK[map_idx]);
+    prefetch_tensormap(&p.tmV[map_idx]);
+    if (kShaped) load_kv();  // on their way while the keys' documents are looked up
   }
+  TileRange qr = qtile_range_keys(geo, Mv, kt * kTileN);
+  DocTiles dt{};
+  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  if (kShaped) {
+    dt = doc_tiles<true>(dm, kt * kTileN, min(kt * kTileN + kTileN, Mv) - 1);
+    qr.kv_begin = dt.begin;
+    qr.kv_end = dt.end;
+  }
+  const int grp = p.grp;
+  const int n_steps = (qr.kv_end - qr.kv_begin) * grp;  // (query tile, head of the group)
+
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
@@ -699,21 +761,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 
   if (warp == 0) {
     // ============================== producer ==============================
-    if (lane == 0 && (!kShaped || n_steps > 0)) {
-      prefetch_tensormap(&p.tmQ[map_idx]);
-      prefetch_tensormap(&p.tmDO[map_idx]);
-      prefetch_tensormap(&p.tmK[map_idx]);
-      prefetch_tensormap(&p.tmV[map_idx]);
-      mbar_arrive_expect_tx(full_kv, 2 * C::kTile);
-      load_tile<D>(smem, &p.tmK[map_idx], full_kv, p, c, g_kv, kt * kTileN, b);
-      load_tile<D>(smem + C::kTile, &p.tmV[map_idx], full_kv, p, c, g_kv, kt * kTileN, b);
-    }
+    if (!kShaped && lane == 0) load_kv();
     int last = -1;
     for (int s = 0; s < n_steps; ++s) {
       const int st = s % S_;
       const uint32_t ph = (uint32_t)(s / S_) & 1u;
       const int qt = qr.kv_begin + s / grp;
       const int h = g_kv * grp + s % grp;
+      auto load_rows = [&]() {
+        uint8_t* qb = smem + C::kRing + st * C::kStageBytes;
+        mbar_arrive_expect_tx(&full[st], 2 * C::kTile);
+        load_tile<D>(qb, &p.tmQ[map_idx], &full[st], p, c, h, qt * kTileM, b);
+        load_tile<D>(qb + C::kTile, &p.tmDO[map_idx], &full[st], p, c, h, qt * kTileM, b);
+      };
+      if (s < S_ && lane == 0) load_rows();
       // lse (log2 units) and Delta of the tile's 128 query rows, loaded into
       // registers before the wait for the stage so their latency overlaps it;
       // rows past the class end get lse = +inf (P = 0)
@@ -729,12 +790,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           dl[u] = p.delta[li];
         }
       }
-      if (s >= S_ && !mbar_wait(&empty[st], ph ^ 1u, p.err, abort_flag)) break;
-      if (lane == 0) {
-        uint8_t* qb = smem + C::kRing + st * C::kStageBytes;
-        mbar_arrive_expect_tx(&full[st], 2 * C::kTile);
-        load_tile<D>(qb, &p.tmQ[map_idx], &full[st], p, c, h, qt * kTileM, b);
-        load_tile<D>(qb + C::kTile, &p.tmDO[map_idx], &full[st], p, c, h, qt * kTileM, b);
+      if (s >= S_) {
+        if (!mbar_wait(&empty[st], ph ^ 1u, p.err, abort_flag)) break;
+        if (lane == 0) load_rows();
       }
       float* vl = vec + st * 2 * kTileM;
 #pragma unroll
@@ -745,8 +803,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       mbar_arrive(&full[st]);
       last = s;
     }
-    if (lane == 0 && *abort_flag && (!kShaped || n_steps > 0)) {
-      // leave no copy writing shared memory behind
+    // leave no copy writing shared memory behind
+    if (kShaped && lane == 0 && n_steps == 0) drain_copies(full_kv, 1, 0, 0);
+    if (lane == 0 && *abort_flag) {
       drain_copies(full_kv, 1, 0, 0);
       drain_copies(full, S_, 0, last);
     }
