@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -100,6 +101,7 @@ struct BwdTcParams {
   const int32_t* cu_docs;
   const int32_t* doc_pre;
   int n_docs;
+  int sort;  // dkdv kernel: the tiles' longest walks first (tile_of_rank)
 };
 
 template <int D>
@@ -354,24 +356,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     tr.kv_end = dt.end;
   }
   const int n_tiles = tr.kv_end - tr.kv_begin;
-  if (kShaped && warp >= 4) {
-    float* part = reinterpret_cast<float*>(smem + C::kVec);
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const uint4 wa = w_do[kShaped ? i : 0], wo = w_o[kShaped ? i : 0];
-      const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xo[4] = {wo.x, wo.y, wo.z, wo.w};
-      float acc = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc = fmaf(__uint_as_float(xa[e] << 16), __uint_as_float(xo[e] << 16), acc);
-        acc = fmaf(__uint_as_float(xa[e] & 0xFFFF0000u), __uint_as_float(xo[e] & 0xFFFF0000u), acc);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      if (lane % kLanes == 0) part[((warp - 4) * kIters + i) * kRows + lane / kLanes] = acc;
-    }
-  }
-
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
@@ -502,7 +486,23 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // units; rows past the class end get P = 0
     float delta = 0.f, lse2 = INFINITY;
     if (kShaped) {
-      const float d = reinterpret_cast<const float*>(smem + C::kVec)[r];
+      float* part = reinterpret_cast<float*>(smem + C::kVec);
+#pragma unroll
+      for (int i = 0; i < kIters; ++i) {
+        const uint4 wa = w_do[kShaped ? i : 0], wo = w_o[kShaped ? i : 0];
+        const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xo[4] = {wo.x, wo.y, wo.z, wo.w};
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc = fmaf(__uint_as_float(xa[e] << 16), __uint_as_float(xo[e] << 16), acc);
+          acc = fmaf(__uint_as_float(xa[e] & 0xFFFF0000u), __uint_as_float(xo[e] & 0xFFFF0000u), acc);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (lane % kLanes == 0) part[((warp - 4) * kIters + i) * kRows + lane / kLanes] = acc;
+      }
+      asm volatile("bar.sync 1, %0;" ::"r"(kGroupsB * 128) : "memory");
+      const float d = part[r];
       if (row_valid) {
         const size_t li = ((size_t)b * p.H + h) * p.N + m_v;
         if (real_row) {
@@ -705,7 +705,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int jt = x;
   int cl = 0;
   while (cl + 1 < p.nclass && p.tile_prefix[cl + 1] <= jt) ++cl;
-  const int kt = jt - p.tile_prefix[cl];
+  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
+                   p.N, p.L, p.R};
+  const int kt = kShaped && p.sort ? tile_of_rank<true>(dm, jt) : jt - p.tile_prefix[cl];
   const int c = p.class0 + cl;
   const Geometry geo = make_geometry(p.N, p.L, p.R, p.d, p.bs);
   const int Mv = p.Mv[cl];
@@ -736,9 +739,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   TileRange qr = qtile_range_keys(geo, Mv, kt * kTileN);
   DocTiles dt{};
-  const DocMask dm{kShaped && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
-                   kShaped && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
-                   p.N, p.L, p.R};
   if (kShaped) {
     dt = doc_tiles<true>(dm, kt * kTileN, min(kt * kTileN + kTileN, Mv) - 1);
     qr.kv_begin = dt.begin;
@@ -1154,6 +1154,12 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
         const long grid = ntiles * B * Hkv;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
+        // (4096 packed tokens with 8 kv heads, 256 CTAs: 161 us in tile order)
+        // and when some walk may be long
+        const long longest =
+            L < 0 || R < 0 ? ntiles : std::min(ntiles, ((long)L + R) / kTileM + 2);
+        p.sort = kShaped && p.cu_docs && p.n_docs <= 31 && ntiles <= 32 && grid > sm_count() &&
+                 longest * p.grp >= 8;
         swa_bwd_dkdv_kernel<D, kShaped, SC><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
       }
       if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;

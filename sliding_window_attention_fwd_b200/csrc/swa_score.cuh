@@ -238,6 +238,40 @@ __device__ __forceinline__ DocTiles doc_tiles(const DocMask& dm, int m0, int m1)
   return t;
 }
 
+// Longest walks first: of the 128-row tiles of a row of tokens (at most 32,
+// lane k looks at tile k, and at most 31 documents), the one whose walk is the
+// rank-th longest.  With packed documents the walks of the tiles differ widely
+// and in no fixed order; started last, a long one is waited for.
+template <bool kQueriesOfKeys>
+__device__ __forceinline__ int tile_of_rank(const DocMask& dm, int rank) {
+  const int lane = threadIdx.x & 31;
+  const int tiles = (dm.N + kTileM - 1) / kTileM;
+  DocTiles t{};
+  t.bound = lane <= dm.n ? dm.clampN(__ldg(dm.cu + lane)) : 0x7fffffff;
+  t.pre = dm.pre && lane < dm.n ? __ldg(dm.pre + lane) : 0;
+  const int c0 = __shfl_sync(0xffffffffu, t.bound, 0);
+  const int cn = __shfl_sync(0xffffffffu, t.bound, dm.n);
+  const int m0 = lane * kTileM, m1 = m0 + kTileM - 1;
+  const int r0 = m0 > c0 ? m0 : c0, r1 = m1 < cn - 1 ? m1 : cn - 1;
+  int lo = -1, hi = -1;
+  for (int k = 0; k <= dm.n; ++k) {
+    const int b = __shfl_sync(0xffffffffu, t.bound, k);
+    if (r0 >= b) lo = k;
+    if (r1 >= b) hi = k;
+  }
+  const DocSpan s0 = span_of_lanes(t, dm.n, lo, r0), s1 = span_of_lanes(t, dm.n, hi, r1);
+  const int a = kQueriesOfKeys ? dm.query_first(s0, r0) : dm.key_first(s0, r0);
+  const int e = kQueriesOfKeys ? dm.query_last(s1, r1) : dm.key_last(s1, r1);
+  const int n = lane >= tiles ? -1 : (r0 > r1 || a > e ? 0 : e / kTileN - a / kTileN + 1);
+  int mine = 0;
+  for (int k = 0; k < tiles; ++k) {
+    const int other = __shfl_sync(0xffffffffu, n, k);
+    mine += other > n || (other == n && k < lane) ? 1 : 0;
+  }
+  const unsigned at = __ballot_sync(0xffffffffu, lane < tiles && mine == rank);
+  return at ? __ffs(at) - 1 : rank;
+}
+
 // The document of this thread's row i, one of the rows of t (a whole
 // converged warp; other rows get none or a document that does not hold them).
 __device__ __forceinline__ DocSpan DocMask::of_thread(const DocTiles& t, int i) const {

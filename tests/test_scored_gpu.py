@@ -123,6 +123,15 @@ def test_two_heads_per_cta(swa, D, cap, bias):
     run(swa, 1, 705, 64, 16, D, 130, 90, cap, bias)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_key_tiles(swa, D):
+    """Packed documents over more key tiles than SMs (their longest walks go first)."""
+    cu = [[0, 700, 701, 900, 1390], [130, 131, 131, 500, 1400]]
+    pre = [[40, 5, 100, 0], [1, 0, 100, 1000]]
+    run(swa, 2, 1400, 16, 8, D, -1, 0, 20.0, False, cu=cu, pre=pre)
+    run(swa, 2, 1400, 16, 8, D, 600, 40, 0.0, True, cu=cu)
+
+
 def test_batch_of_different_documents(swa):
     cu = [[0, 100, 300], [10, 10, 290], [0, 0, 0]]
     pre = [[0, 40], [7, 1000], [-3, 5]]
