@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     swa_bwd_dq_kernel(const __grid_constant__ BwdTcParams p) {
   using C = BCfg<D>;
   constexpr int S_ = C::kStages;
+  if (kShaped) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -762,6 +763,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 0) {
     // ============================== producer ==============================
     if (!kShaped && lane == 0) load_kv();
+    // the dq kernel, which this one may have been started beside, has written
+    // every Delta (every CTA waits, so that this grid's end is also its end)
+    if (kShaped) asm volatile("griddepcontrol.wait;" ::: "memory");
     int last = -1;
     for (int s = 0; s < n_steps; ++s) {
       const int st = s % S_;
@@ -1079,8 +1083,9 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
   const Geometry geo = make_geometry(N, L, R, d, bs);
   const bool block_mode = geo.bs > 1;
   // two passes over the class chunks: every Delta is written (dq kernel)
-  // before any is read (dkdv kernel)
-  for (int pass = 0; pass < 2; ++pass) {
+  // before any is read (dkdv kernel); shaped, there is one class, and the
+  // dkdv kernel is scheduled while the dq kernel's last CTAs run
+  for (int pass = 0; pass < (kShaped ? 1 : 2); ++pass) {
     for (int c0 = 0; c0 < geo.nclass; c0 += kMaxClassesB) {
       BwdTcParams p;
       std::memset(&p, 0, sizeof(p));
@@ -1150,7 +1155,8 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
         swa_bwd_dq_kernel<D, kShaped, SC><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
-      } else {
+      }
+      if (kShaped || pass == 1) {
         const long grid = ntiles * B * Hkv;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
@@ -1160,7 +1166,18 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
             L < 0 || R < 0 ? ntiles : std::min(ntiles, ((long)L + R) / kTileM + 2);
         p.sort = kShaped && p.cu_docs && p.n_docs <= 31 && ntiles <= 32 && grid > sm_count() &&
                  longest * p.grp >= 8;
-        swa_bwd_dkdv_kernel<D, kShaped, SC><<<(unsigned)grid, kThreadsB, C::kAlloc, stream>>>(p);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(kThreadsB);
+        cfg.dynamicSmemBytes = C::kAlloc;
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = kShaped ? 1 : 0;
+        if (cudaLaunchKernelEx(&cfg, swa_bwd_dkdv_kernel<D, kShaped, SC>, p) != cudaSuccess)
+          return SWA_ERR_CUDA;
       }
       if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
     }
