@@ -271,6 +271,11 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
               ok = false;
               break;
             }
+#ifdef SWA_TEST_WITHHOLD_TILE
+            // failure-detection test build only: this K tile is never loaded,
+            // so the issuer's bounded wait for it runs out
+            if (j == 2 * SWA_TEST_WITHHOLD_TILE) continue;
+#endif
             mbar_arrive_expect_tx(&full[st], C::kTile);
             for (int hh = 0; hh < 2; ++hh)
               for (int cc = 0; cc < D / 64; ++cc)
@@ -280,7 +285,12 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
         }
       }
       if (*abort_flag) {  // leave no copy writing shared memory behind
-        drain_copies(full, S_, 0, j - 1);
+#ifdef SWA_TEST_WITHHOLD_TILE
+        const int skip = 2 * SWA_TEST_WITHHOLD_TILE;
+#else
+        const int skip = -1;
+#endif
+        drain_copies(full, S_, 0, j - 1, skip);
         drain_copies(q_full, 2, 0, last_q);
       }
     }

@@ -142,6 +142,8 @@ SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int ma
   const long long fill = (2 * sms + (long long)B * Hkv - 1) / ((long long)B * Hkv);
   const long long most = (tail + 255) / 256;
   if (own < fill) own = fill < most ? fill : most;
+  // (and no more than four items per CTA need: the rest would only be merged)
+  if (own > 4 * fill) own = 4 * fill;
   pl.own_parts = (int)(own < 1 ? 1 : own);
   const long long keys = (tail + pl.own_parts - 1) / pl.own_parts;
   pl.part_keys = (int)((keys + kTileN - 1) / kTileN * kTileN);

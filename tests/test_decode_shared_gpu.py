@@ -165,6 +165,22 @@ def test_without_a_prefix_it_is_the_paged_decode(swa):
     assert (a.float() - b.float()).abs().max() <= 4 * R.HALF_BF16 * a.float().abs().max()
 
 
+def test_large_offsets(swa):
+    """A page pool whose element offsets pass 2^32, its last pages in use."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    H, Hkv, D, page, P, W = 8, 8, 128, 64, 150, 100
+    q, k0, v0, ptab, table, pos = build(P, [200, 333], H, Hkv, D, page)
+    rows = ((1 << 32) // (Hkv * D) + k0.shape[0]) // page * page
+    kp, vp = (torch.zeros(rows, Hkv, D, dtype=BF, device="cuda") for _ in range(2))
+    kp[-k0.shape[0]:], vp[-v0.shape[0]:] = k0, v0
+    want = swa.swa_decode_shared(q, k0, v0, ptab.cuda(), P, table.cuda(), pos.cuda(), page, W)
+    up = (rows - k0.shape[0]) // page
+    ptab, table = torch.where(ptab < 0, ptab, ptab + up), torch.where(table < 0, table, table + up)
+    got = swa.swa_decode_shared(q, kp, vp, ptab.cuda(), P, table.cuda(), pos.cuda(), page, W)
+    assert torch.equal(got, want)
+
+
 def test_captured_and_at_once(swa):
     """Two captured decodes of different sizes replayed in turn; two calls at once."""
     sides, st = [], [torch.cuda.Stream() for _ in range(2)]
