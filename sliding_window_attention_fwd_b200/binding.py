@@ -2,7 +2,7 @@
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib
 import os
 
 import torch
@@ -16,6 +16,7 @@ if not os.path.exists(_LIB_PATH):
         "`python -m sliding_window_attention_fwd_b200.build` (nvcc, sm_100a)")
 
 _lib = ctypes.CDLL(_LIB_PATH)
+_calls = importlib.import_module("._torch_calls", __package__)  # csrc/swa_torch.cpp, built with it
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -98,6 +99,11 @@ class SwaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {swa_status_string(status)} ({status})")
+
+
+_calls.init(SwaError, *(ctypes.cast(getattr(_lib, _n), _P).value for _n in (
+    "swa_forward_scored", "swa_backward_scored", "swa_rope_append_paged", "swa_decode_shared",
+    "swa_decode_shared_workspace_bytes")))
 
 
 def library_path() -> str:
@@ -442,86 +448,7 @@ def swa_append(q, k_new, v_new, k_ring, v_ring, pos0, out=None, lse=None, scale=
 
 
 # The calls below are made once per layer and token, where the host's time
-# counts: their checks are first made in one pass without building messages
-# (_ready, dtypes and shapes), and only if that fails by the functions above,
-# which say what is wrong.
-
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-
-
-def _ready(dev, *tensors):
-    """Whether every tensor (None skipped) is contiguous and on CUDA device `dev`."""
-    if dev < 0:
-        return False
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            return False
-    return True
-
-
-# (of a CUDA tensor's device, so CUDA is initialised)
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _run(dev, stream, name, *args):
-    """Calls the library's `name` with the stream appended, on device `dev`."""
-    fn = getattr(_lib, name)
-    if dev == _device():
-        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _stream(stream))
-    if status != 0:
-        raise SwaError(status, name)
-
-
-def _scratch(n, dtype, dev, stream):
-    """Uninitialised device memory that torch's allocator reuses in the order of
-    `stream` (as _stream takes it)."""
-    if stream is None:
-        return torch.empty(n, dtype=dtype, device=dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=dtype, device=dev)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _scored_common(q, k, v, out, lse, softcap, slopes, cu_docs, prefix):
-    """Checks a scored call's tensors.  Returns the sizes and its swa_score block."""
-    B, N, H, D = q.shape
-    Hkv = k.shape[2]
-    n = 0
-    ok = (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and out.dtype is _BF16
-          and k.shape == (B, N, Hkv, D) and v.shape == k.shape and out.shape == q.shape)
-    if lse is not None:
-        ok = ok and lse.dtype is _F32 and lse.shape == (B, H, N)
-    if slopes is not None:
-        ok = ok and slopes.dtype is _F32 and slopes.shape == (H,)
-    if cu_docs is not None:
-        n = cu_docs.shape[-1] - 1
-        ok = ok and cu_docs.dtype is _I32 and cu_docs.shape == (B, n + 1) and n > 0
-    if prefix is not None:
-        ok = ok and cu_docs is not None and prefix.dtype is _I32 and prefix.shape == (B, n)
-    if not (ok and _ready(q.get_device(), q, k, v, out, lse, slopes, cu_docs, prefix)):
-        _fwd_common(q, k, v, out, lse, None, _BF16)
-        if slopes is not None:
-            _need(slopes, "slopes", _F32, 1, (H,))
-        if cu_docs is not None:
-            _need(cu_docs, "cu_docs", _I32, 2)
-            if cu_docs.shape[0] != B or n < 1:
-                raise ValueError(f"cu_docs: expected [{B}, documents + 1], got "
-                                 f"{tuple(cu_docs.shape)}")
-        if prefix is not None:
-            if cu_docs is None:
-                raise ValueError("prefix needs cu_docs")
-            _need(prefix, "prefix", _I32, 2, (B, n))
-        _placed(q, slopes=slopes, cu_docs=cu_docs, prefix=prefix)
-    return B, N, H, Hkv, D, SwaScore(softcap, _at(slopes), _at(cu_docs), _at(prefix), n)
+# counts: their tensors are checked and handed on in csrc/swa_torch.cpp.
 
 
 def swa_forward_scored(q, k, v, out=None, lse=None, win_left=-1, win_right=-1, softcap=0.0,
@@ -529,16 +456,8 @@ def swa_forward_scored(q, k, v, out=None, lse=None, win_left=-1, win_right=-1, s
     """bf16 forward with shaped scores (C: swa_forward_scored): tanh cap, distance
     bias slopes [H] fp32, packed documents cu_docs [B, n + 1] int32 with prefix
     lengths [B, n] int32.  Returns out."""
-    if q.dim() != 4 or k.dim() != 4:
-        _fwd_common(q, k, v, out, lse, None, _BF16)
-    if out is None:
-        out = torch.empty_like(q)
-    B, N, H, Hkv, D, sc = _scored_common(q, k, v, out, lse, softcap, slopes, cu_docs, prefix)
-    if B > 0 and N > 0:  # (an empty tensor has no address to check)
-        _run(q.get_device(), stream, "swa_forward_scored", q.data_ptr(), k.data_ptr(),
-             v.data_ptr(), out.data_ptr(), _at(lse), B, H, Hkv, N, D, win_left, win_right,
-             ctypes.addressof(sc), scale)
-    return out
+    return _calls.forward_scored(q, k, v, out, lse, win_left, win_right, softcap, slopes, cu_docs,
+                                 prefix, scale, stream)
 
 
 def swa_backward_scored(q, k, v, out, dout, lse, win_left=-1, win_right=-1, softcap=0.0,
@@ -546,43 +465,8 @@ def swa_backward_scored(q, k, v, out, dout, lse, win_left=-1, win_right=-1, soft
                         dv=None, stream=None):
     """Gradients (dq, dk, dv) of swa_forward_scored (C: swa_backward_scored); out
     and lse are the forward's outputs for the same arguments."""
-    if out is None or lse is None:
-        raise ValueError("out and lse (from the forward) are required")
-    if q.dim() != 4 or k.dim() != 4:
-        _fwd_common(q, k, v, out, lse, None, _BF16)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    dev = q.get_device()
-    B, N, H, Hkv, D, sc = _scored_common(q, k, v, out, lse, softcap, slopes, cu_docs, prefix)
-    if not (dout.dtype is _BF16 and dq.dtype is _BF16 and dk.dtype is _BF16 and dv.dtype is _BF16
-            and dout.shape == q.shape and dq.shape == q.shape and dk.shape == k.shape
-            and dv.shape == k.shape and _ready(dev, dout, dq, dk, dv)):
-        for t, n, ref in ((dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-            _need(t, n, _BF16, 4, ref.shape)
-        _placed(q, dout=dout, dq=dq, dk=dk, dv=dv)
-    if B > 0 and N > 0:
-        delta = _scratch(B * H * N, _F32, q.device, stream)
-        _run(dev, stream, "swa_backward_scored", q.data_ptr(), k.data_ptr(), v.data_ptr(),
-             out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-             dv.data_ptr(), delta.data_ptr(), B, H, Hkv, N, D, win_left, win_right,
-             ctypes.addressof(sc), scale)
-    return dq, dk, dv
-
-
-def _token_rows(t, name, dev):
-    """t [T, heads, D]: dense rows, any stride between tokens -> that stride."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name}: must be a CUDA tensor on the queries' device")
-    T, heads, D = t.shape
-    between, row, one = t.stride()
-    if one != 1 or (row != D and heads > 1):
-        raise ValueError(f"{name}: the rows of a token must be contiguous")
-    if T <= 1:
-        return heads * D
-    if between < heads * D:
-        raise ValueError(f"{name}: tokens overlap")
-    return between
+    return _calls.backward_scored(q, k, v, out, dout, lse, win_left, win_right, softcap, slopes,
+                                  cu_docs, prefix, scale, dq, dk, dv, stream)
 
 
 def swa_rope_append_paged(q, k, v, inv_freq, cu, pos0, block_table, k_pages, v_pages, page_size,
@@ -592,53 +476,14 @@ def swa_rope_append_paged(q, k, v, inv_freq, cu, pos0, block_table, k_pages, v_p
     tokens); inv_freq [rot / 2] fp32; cu [B + 1] int32; pos0 [B] int64;
     block_table [B, max_pages] int32; k_pages/v_pages [num_pages * page_size, Hkv,
     D], updated in place.  Returns q_out [T, H, D], the rotated queries."""
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if not (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and k_pages.dtype is _BF16
-            and v_pages.dtype is _BF16 and q_out.dtype is _BF16 and inv_freq.dtype is _F32
-            and cu.dtype is _I32 and pos0.dtype is _I64 and block_table.dtype is _I32
-            and q.dim() == 3 and k_pages.dim() == 3 and inv_freq.dim() == 1 and cu.dim() == 1
-            and pos0.dim() == 1 and block_table.dim() == 2):
-        for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages"),
-                     (q_out, "q_out")):
-            _need(t, n, _BF16, 3)
-        _need(inv_freq, "inv_freq", _F32, 1)
-        _need(cu, "cu", _I32, 1)
-        _need(pos0, "pos0", _I64, 1)
-        _need(block_table, "block_table", _I32, 2)
-    T, H, D = q.shape
-    rows, Hkv, Dk = k_pages.shape
-    B, max_pages = block_table.shape
-    if (k.shape != (T, Hkv, D) or v.shape != k.shape or Dk != D or v_pages.shape != k_pages.shape
-            or q_out.shape != q.shape or cu.shape[0] != B + 1 or pos0.shape[0] != B
-            or page_size < 1 or rows % page_size != 0):
-        raise ValueError("k/v [T, Hkv, D], k_pages/v_pages [num_pages * page_size, Hkv, D], "
-                         "cu [B + 1], pos0 [B], block_table [B, *], q_out like q")
-    dev = q.get_device()
-    strides = (_token_rows(q, "q", dev), _token_rows(k, "k", dev), _token_rows(v, "v", dev),
-               _token_rows(q_out, "q_out", dev))
-    if not _ready(dev, inv_freq, cu, pos0, block_table, k_pages, v_pages):
-        _placed(q, inv_freq=inv_freq, cu=cu, pos0=pos0, block_table=block_table, k_pages=k_pages,
-                v_pages=v_pages)
-    if T > 0 and B > 0:
-        _run(dev, stream, "swa_rope_append_paged", q.data_ptr(), k.data_ptr(), v.data_ptr(),
-             strides[0], strides[1], strides[2], inv_freq.data_ptr(), 2 * inv_freq.shape[0],
-             int(interleaved), cu.data_ptr(), pos0.data_ptr(), block_table.data_ptr(),
-             q_out.data_ptr(), strides[3], k_pages.data_ptr(), v_pages.data_ptr(), T, B, H, Hkv,
-             D, page_size, rows // page_size, max_pages)
-    return q_out
+    return _calls.rope_append_paged(q, k, v, inv_freq, cu, pos0, block_table, k_pages, v_pages,
+                                    page_size, q_out, interleaved, stream)
 
 
 def swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail) -> int:
     """Bytes of workspace swa_decode_shared takes for these sizes (C:
     swa_decode_shared_workspace_bytes)."""
     return _lib.swa_decode_shared_workspace_bytes(B, H, Hkv, D, n_prefix, W, max_tail)
-
-
-@functools.lru_cache(maxsize=256)
-def _shared_workspace(dev, *sizes):
-    with torch.cuda.device(dev):
-        return _lib.swa_decode_shared_workspace_bytes(*sizes)
 
 
 def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, pos, page_size, W,
@@ -651,49 +496,9 @@ def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, 
     prefix (default: what the block table has room for), which only sets how
     the work is split.  The workspace comes from torch's allocator.  Returns out
     [B, H, D]."""
-    if out is None:
-        out = torch.empty_like(q)
-    if not (q.dtype is _BF16 and k_pages.dtype is _BF16 and v_pages.dtype is _BF16
-            and out.dtype is _BF16 and prefix_table.dtype is _I32 and block_table.dtype is _I32
-            and pos.dtype is _I64 and q.dim() == 3 and k_pages.dim() == 3
-            and prefix_table.dim() == 1 and block_table.dim() == 2 and pos.dim() == 1
-            and out.shape == q.shape):
-        for t, n in ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages")):
-            _need(t, n, _BF16, 3)
-        _need(out, "out", _BF16, 3, q.shape)
-        _need(prefix_table, "prefix_table", _I32, 1)
-        _need(block_table, "block_table", _I32, 2)
-        _need(pos, "pos", _I64, 1)
-    B, H, D = q.shape
-    rows, Hkv, Dk = k_pages.shape
-    max_pages = block_table.shape[1]
-    if (Dk != D or v_pages.shape != k_pages.shape or pos.shape[0] != B
-            or block_table.shape[0] != B or page_size < 1 or rows % page_size != 0):
-        raise ValueError("k_pages/v_pages [num_pages * page_size, Hkv, D], block_table [B, *], "
-                         "pos [B]")
-    if n_prefix < 0 or prefix_table.shape[0] * page_size < n_prefix:
-        raise ValueError("prefix_table: expected the pages of n_prefix >= 0 positions")
-    if lse is not None:
-        _need(lse, "lse", _F32, 2, (B, H))
-    if slopes is not None:
-        _need(slopes, "slopes", _F32, 1, (H,))
-    dev = q.get_device()
-    if not _ready(dev, q, k_pages, v_pages, prefix_table, block_table, pos, out, lse, slopes):
-        _placed(q, q=q, k_pages=k_pages, v_pages=v_pages, prefix_table=prefix_table,
-                block_table=block_table, pos=pos, out=out, lse=lse, slopes=slopes)
-    if B == 0:
-        return out
-    if max_tail is None:
-        max_tail = max_pages * page_size - n_prefix
-    max_tail = max(0, min(max_tail, 2 ** 31 - 1))
-    nbytes = _shared_workspace(dev, B, H, Hkv, D, n_prefix, W, max_tail)
-    ws = _scratch(max(16, nbytes), torch.uint8, q.device, stream)
-    _run(dev, stream, "swa_decode_shared", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-         out.data_ptr(), _at(lse), prefix_table.data_ptr() if n_prefix else None, n_prefix,
-         block_table.data_ptr(), pos.data_ptr(), B, H, Hkv, D, page_size, rows // page_size,
-         max_pages, W, int(keep_prefix), max_tail, softcap, _at(slopes), scale, ws.data_ptr(),
-         ws.numel())
-    return out
+    return _calls.decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, pos,
+                                page_size, W, out, lse, keep_prefix, max_tail, softcap, slopes,
+                                scale, stream)
 
 
 def swa_device_error(stream=None) -> int:

@@ -1,15 +1,20 @@
-"""Builds the CUDA library libswa.so in-tree with nvcc for sm_100a."""
+"""Builds, in-tree, the CUDA library libswa.so with nvcc for sm_100a and the binding's
+extension module (csrc/swa_torch.cpp) with g++."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libswa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+CALLS_SRC = os.path.join(CSRC, "swa_torch.cpp")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -29,10 +34,26 @@ def deps():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in deps())
+    for built, needs in ((LIB, deps()), (CALLS, [CALLS_SRC, os.path.join(INCLUDE, "swa.h")])):
+        if not os.path.exists(built):
+            return True
+        if any(os.path.getmtime(p) > os.path.getmtime(built) for p in needs):
+            return True
+    return False
+
+
+def calls_command():
+    """g++ command of the extension module.  torch and its libraries are loaded
+    before it is imported, so it carries no path to them."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(torch_dir, "include"),
+            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", CALLS,
+            "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str | None:
@@ -40,16 +61,16 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str | None:
     if not srcs:
         return None
     if force or stale():
-        # every source in its own nvcc process, then the link
+        # every source in its own process, then the library's link
         flags = [f for f in NVCC_FLAGS if f != "-shared"]
         with tempfile.TemporaryDirectory() as tmp:
-            objs, procs = [], []
-            for src in srcs:
-                objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
-                cmd = ["nvcc", *flags, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", objs[-1]]
-                if verbose:
+            objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in srcs]
+            cmds = [["nvcc", *flags, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+                    for src, obj in zip(srcs, objs)] + [calls_command()]
+            if verbose:
+                for cmd in cmds:
                     print(" ".join(cmd))
-                procs.append((cmd, subprocess.Popen(cmd)))
+            procs = [(cmd, subprocess.Popen(cmd)) for cmd in cmds]
             failed = [cmd for cmd, proc in procs if proc.wait() != 0]
             if failed:
                 raise subprocess.CalledProcessError(1, failed[0])

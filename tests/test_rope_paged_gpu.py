@@ -179,3 +179,35 @@ def test_captured_and_on_a_stream(swa):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(k2, kp) and torch.equal(v2, vp)
+
+
+def test_token_strides_refused(swa):
+    q, k, v, cu, pos0, table, kp, vp = make([5, 6], [60, 3], 4, 2, 64, 64, True)
+    inv = freqs(64)
+
+    def call(**kw):
+        a = dict(q=q, k=k, v=v, inv_freq=inv, cu=cu, pos0=pos0, block_table=table, k_pages=kp,
+                 v_pages=vp, page_size=64) | kw
+        return swa.swa_rope_append_paged(**a)
+    wide = torch.zeros(11, 4, 128, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q=wide[:, :, :64])
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q=wide[:, :, ::2])
+    with pytest.raises(ValueError, match="overlap"):
+        call(q=q[:1].expand(11, 4, 64))
+    with pytest.raises(ValueError, match="CUDA"):
+        call(q_out=torch.zeros(11, 4, 64, dtype=BF))
+    with pytest.raises(ValueError, match="CUDA"):
+        call(cu=cu.cpu())
+    with pytest.raises(swa.SwaError):  # tokens not on 16-byte boundaries
+        odd = torch.zeros(11, 4 * 64 + 4, dtype=BF, device="cuda")
+        call(q=odd[:, :256].unflatten(1, (4, 64)))
+    with pytest.raises(swa.SwaError):
+        call(inv_freq=inv[:12].contiguous())
+    one = q[:1].as_strided((1, 4, 64), (3, 64, 1))  # one token: its stride does not matter
+    call(q=one, k=k[:1], v=v[:1], cu=torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda"))
+    none = q[:0]  # nothing to do
+    assert call(q=none, k=k[:0], v=v[:0]).shape == (0, 4, 64)
+    torch.cuda.synchronize()
+    assert swa.swa_device_error() == 0

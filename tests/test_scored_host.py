@@ -113,146 +113,118 @@ def test_shared_workspace_grows_with_the_call():
 
 
 # ------------------------------------------------------------------ the binding
+# CPU tensors of the right shapes get as far as the placement check, which shows that
+# the shape checks took them; a wrong argument is named before that.
+CUDA_ONLY = "must be a (contiguous )?CUDA tensor"
+
+
 def t(*shape, dtype=BF):
     return torch.zeros(shape, dtype=dtype)
 
 
-@pytest.fixture
-def lib(monkeypatch):
-    class Recorder:
-        def __init__(self):
-            self.calls = {}
-
-        def __getattr__(self, name):
-            if name.endswith("_bytes"):
-                return lambda *a: 4096
-
-            def fn(*args):
-                self.calls[name] = [a.value if isinstance(a, ctypes.c_void_p) else a for a in args]
-                return 0
-            return fn
-    rec = Recorder()
-    monkeypatch.setattr(b, "_lib", rec)
-    monkeypatch.setattr(b, "_placed", lambda ref, **kw: None)
-    monkeypatch.setattr(b, "_token_rows", lambda x, n, dev: x.stride(0))
-    monkeypatch.setattr(b, "_device", lambda: -1)  # what CPU tensors say
-    monkeypatch.setattr(b, "_raw_stream", lambda d: "STREAM")
-    return rec
+def score_args():
+    return dict(q=t(2, 50, 8, 64), k=t(2, 50, 2, 64), v=t(2, 50, 2, 64), out=t(2, 50, 8, 64),
+                lse=t(2, 8, 50, dtype=F32), win_left=7, win_right=0, softcap=20.0,
+                slopes=t(8, dtype=F32), cu_docs=t(2, 4, dtype=I32), prefix=t(2, 3, dtype=I32))
 
 
-def test_scored_marshalling(lib):
-    q, k, v, out, lse = t(2, 50, 8, 64), t(2, 50, 2, 64), t(2, 50, 2, 64), t(2, 50, 8, 64), \
-        t(2, 8, 50, dtype=F32)
-    sl, cu, pre = t(8, dtype=F32), t(2, 4, dtype=I32), t(2, 3, dtype=I32)
-    seen = {}
-
-    def keep(name):
-        def fn(*a):
-            a = [x.value if isinstance(x, ctypes.c_void_p) else x for x in a]
-            sc = ctypes.cast(a[-3], ctypes.POINTER(b.SwaScore))[0]
-            seen[name] = (a[:-3] + a[-2:], [getattr(sc, f[0]) for f in b.SwaScore._fields_])
-            return 0
-        return fn
-    lib.swa_forward_scored = keep("f")
-    lib.swa_backward_scored = keep("b")
-    want = [20.0, sl.data_ptr(), cu.data_ptr(), pre.data_ptr(), 3]
-    b.swa_forward_scored(q, k, v, out, lse, 7, 0, 20.0, sl, cu, pre, 0.5)
-    assert seen["f"] == ([x.data_ptr() for x in (q, k, v, out, lse)]
-                         + [2, 8, 2, 50, 64, 7, 0, 0.5, "STREAM"], want)
-    dq, dk, dv = b.swa_backward_scored(q, k, v, out, q, lse, 7, 0, 20.0, sl, cu, pre, 0.5)
-    got, sc = seen["b"]
-    assert sc == want
-    assert got[:9] == [x.data_ptr() for x in (q, k, v, out, q, lse, dq, dk, dv)]
-    assert got[10:] == [2, 8, 2, 50, 64, 7, 0, 0.5, "STREAM"]
-    b.swa_forward_scored(q, k, v)
-    assert seen["f"][1] == [0.0, None, None, None, 0]
+SCORE_BAD = [
+    dict(q=t(2, 50, 8, 32)), dict(q=t(50, 8, 64)), dict(q=t(2, 50, 8, 64, dtype=F32)),
+    dict(k=t(2, 49, 2, 64)), dict(k=t(2, 50, 64)), dict(v=t(2, 50, 4, 64)), dict(out=t(2, 50, 2, 64)),
+    dict(lse=t(2, 50, 8, dtype=F32)), dict(lse=t(2, 8, 50)), dict(slopes=t(7, dtype=F32)),
+    dict(slopes=t(8)), dict(cu_docs=t(2, 1, dtype=I32), prefix=None), dict(cu_docs=t(1, 4, dtype=I32)),
+    dict(cu_docs=t(2, 4, dtype=I64)), dict(cu_docs=None), dict(prefix=t(2, 4, dtype=I32)),
+]
 
 
-def test_rope_marshalling(lib):
-    qkv = t(9, 8 * 64)
-    q, k, v = (x.unflatten(1, (-1, 64)) for x in qkv.split((256, 128, 128), 1))
-    inv, cu, pos0, tab = t(16, dtype=F32), t(4, dtype=I32), t(3, dtype=I64), t(3, 5, dtype=I32)
-    kp, vp = t(7 * 48, 2, 64), t(7 * 48, 2, 64)
-    out = b.swa_rope_append_paged(q, k, v, inv, cu, pos0, tab, kp, vp, 48, interleaved=True)
-    assert lib.calls["swa_rope_append_paged"] == [
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), 512, 512, 512, inv.data_ptr(), 32, 1,
-        cu.data_ptr(), pos0.data_ptr(), tab.data_ptr(), out.data_ptr(), 256, kp.data_ptr(),
-        vp.data_ptr(), 9, 3, 4, 2, 64, 48, 7, 5, "STREAM"]
+@pytest.mark.parametrize("bad", SCORE_BAD)
+def test_scored_tensors_checked(bad):
+    with pytest.raises(ValueError, match="expected|needs cu_docs"):
+        b.swa_forward_scored(**(score_args() | bad))
+    with pytest.raises(ValueError, match="expected|needs cu_docs"):
+        b.swa_backward_scored(dout=t(2, 50, 8, 64), **(score_args() | bad))
 
 
-def test_shared_marshalling(lib):
-    q, kp, vp = t(3, 8, 128), t(5 * 64, 2, 128), t(5 * 64, 2, 128)
-    ptab, tab, pos, lse, sl = t(2, dtype=I32), t(3, 4, dtype=I32), t(3, dtype=I64), \
-        t(3, 8, dtype=F32), t(8, dtype=F32)
-    out = b.swa_decode_shared(q, kp, vp, ptab, 100, tab, pos, 64, 33, lse=lse, keep_prefix=False,
-                              softcap=5.0, slopes=sl, scale=0.25)
-    got = lib.calls["swa_decode_shared"]
-    assert got[:22] == [q.data_ptr(), kp.data_ptr(), vp.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                        ptab.data_ptr(), 100, tab.data_ptr(), pos.data_ptr(), 3, 8, 2, 128, 64, 5,
-                        4, 33, 0, 156, 5.0, sl.data_ptr(), 0.25]
-    assert got[23:] == [4096, "STREAM"]
+def test_scored_placement_checked():
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        b.swa_forward_scored(**score_args())
+    args = score_args() | dict(dout=t(2, 50, 8, 64))
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        b.swa_backward_scored(**args)
+    with pytest.raises(ValueError, match="required"):
+        b.swa_backward_scored(**(args | dict(out=None)))
+    with pytest.raises(ValueError, match="required"):
+        b.swa_backward_scored(**(args | dict(lse=None)))
+    with pytest.raises(ValueError, match="expected a torch tensor"):
+        b.swa_forward_scored(**(score_args() | dict(q=[1.0])))
+    e = torch.empty(2, 0, 4, 64, dtype=BF)  # also where there is nothing to do
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        b.swa_forward_scored(e, e, e)
+
+
+def rope_args():
+    return dict(q=t(9, 4, 64), k=t(9, 2, 64), v=t(9, 2, 64), inv_freq=t(16, dtype=F32),
+                cu=t(4, dtype=I32), pos0=t(3, dtype=I64), block_table=t(3, 5, dtype=I32),
+                k_pages=t(96, 2, 64), v_pages=t(96, 2, 64), page_size=48, q_out=t(9, 4, 64))
 
 
 @pytest.mark.parametrize("bad", [
-    dict(slopes=t(7, dtype=F32)), dict(slopes=t(8)), dict(cu_docs=t(2, 1, dtype=I32)),
-    dict(cu_docs=t(1, 4, dtype=I32)), dict(cu_docs=t(2, 4, dtype=I64)),
-    dict(prefix=t(2, 3, dtype=I32)),
-    dict(cu_docs=t(2, 4, dtype=I32), prefix=t(2, 4, dtype=I32)),
+    dict(k=t(8, 2, 64)), dict(v=t(9, 1, 64)), dict(cu=t(3, dtype=I32)), dict(cu=t(4, dtype=I64)),
+    dict(page_size=50), dict(page_size=0), dict(page_size=-48), dict(v_pages=t(96, 2, 32)),
+    dict(k_pages=t(96, 4, 64), v_pages=t(96, 4, 64)), dict(inv_freq=t(16)),
+    dict(inv_freq=t(2, 8, dtype=F32)), dict(pos0=t(3, dtype=I32)),
+    dict(block_table=t(2, 5, dtype=I32)), dict(block_table=t(15, dtype=I32)),
+    dict(q_out=t(9, 2, 64)), dict(q=t(9, 256)),
 ])
-def test_binding_refuses_score_arrays(lib, bad):
-    q, k, v = t(2, 50, 8, 64), t(2, 50, 2, 64), t(2, 50, 2, 64)
+def test_rope_tensors_checked(bad):
+    with pytest.raises(ValueError, match="expected"):
+        b.swa_rope_append_paged(**(rope_args() | bad))
+
+
+def test_rope_placement_checked():
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        b.swa_rope_append_paged(**rope_args())
+
+
+def shared_args():
+    return dict(q=t(3, 8, 128), k_pages=t(320, 2, 128), v_pages=t(320, 2, 128),
+                prefix_table=t(2, dtype=I32), n_prefix=100, block_table=t(3, 4, dtype=I32),
+                pos=t(3, dtype=I64), page_size=64, W=33, out=t(3, 8, 128),
+                lse=t(3, 8, dtype=F32), slopes=t(8, dtype=F32))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_prefix=129), dict(n_prefix=-1), dict(page_size=96), dict(page_size=0),
+    dict(block_table=t(2, 4, dtype=I32)), dict(block_table=t(3, 4, dtype=I64)),
+    dict(v_pages=t(320, 4, 128)), dict(k_pages=t(320, 2, 64), v_pages=t(320, 2, 64)),
+    dict(pos=t(2, dtype=I64)), dict(pos=t(3, dtype=I32)), dict(out=t(3, 8, 64)),
+    dict(lse=t(8, 3, dtype=F32)), dict(slopes=t(2, dtype=F32)), dict(prefix_table=t(2, dtype=I64)),
+    dict(q=t(3, 8, 128, dtype=F32)),
+])
+def test_shared_tensors_checked(bad):
+    with pytest.raises(ValueError, match="expected"):
+        b.swa_decode_shared(**(shared_args() | bad))
+
+
+def test_shared_placement_checked():
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        b.swa_decode_shared(**shared_args())
+
+
+@pytest.mark.parametrize("call,args,bad", [
+    (b.swa_rope_append_paged, rope_args, dict(page_size="48")),
+    (b.swa_decode_shared, shared_args, dict(W=1.5)),
+    (b.swa_decode_shared, shared_args, dict(n_prefix=None)),
+])
+def test_numbers_of_the_wrong_kind(call, args, bad):
+    with pytest.raises(TypeError):
+        call(**(args() | bad))
+
+
+@pytest.mark.parametrize("bad", [dict(W=2 ** 31), dict(page_size=2 ** 40), dict(n_prefix=-2 ** 31 - 1)])
+def test_numbers_out_of_range(bad):
     with pytest.raises(ValueError):
-        b.swa_forward_scored(q, k, v, **bad)
-    with pytest.raises(ValueError):
-        b.swa_backward_scored(q, k, v, q, q, t(2, 8, 50, dtype=F32), **bad)
-    assert not lib.calls
-
-
-def test_binding_refuses_shapes(lib):
-    q, kp = t(3, 8, 128), t(5 * 64, 2, 128)
-    ptab, tab, pos = t(2, dtype=I32), t(3, 4, dtype=I32), t(3, dtype=I64)
-    for args in ((q, kp, kp, ptab, 129, tab, pos, 64, 33), (q, kp, kp, ptab, -1, tab, pos, 64, 33),
-                 (q, kp, kp, ptab, 100, tab, pos, 96, 33), (q, kp, kp, ptab, 100, tab[:2], pos, 64, 33),
-                 (q, kp, t(5 * 64, 4, 128), ptab, 100, tab, pos, 64, 33),
-                 (q, kp, kp, ptab, 100, tab, pos, 0, 33)):
-        with pytest.raises(ValueError):
-            b.swa_decode_shared(*args)
-    r = dict(q=t(9, 4, 64), k=t(9, 2, 64), v=t(9, 2, 64), inv_freq=t(16, dtype=F32),
-             cu=t(4, dtype=I32), pos0=t(3, dtype=I64), block_table=t(3, 5, dtype=I32),
-             k_pages=t(96, 2, 64), v_pages=t(96, 2, 64), page_size=48)
-    for bad in (dict(k=t(8, 2, 64)), dict(v=t(9, 1, 64)), dict(cu=t(3, dtype=I32)),
-                dict(page_size=50), dict(page_size=0), dict(v_pages=t(96, 2, 32)),
-                dict(inv_freq=t(16)), dict(pos0=t(3, dtype=I32)), dict(block_table=t(2, 5, dtype=I32)),
-                dict(q_out=t(9, 2, 64))):
-        with pytest.raises(ValueError):
-            b.swa_rope_append_paged(**(r | bad))
-    assert not lib.calls
-
-
-def test_binding_checks_token_strides():
-    class OnGpu:  # a CUDA tensor's shape and strides without a GPU
-        def __init__(self, shape, stride):
-            self.shape, self._s = shape, stride
-
-        def get_device(self):
-            return 0
-
-        def stride(self):
-            return self._s
-    assert b._token_rows(OnGpu((4, 2, 64), (512, 64, 1)), "q", 0) == 512
-    assert b._token_rows(OnGpu((1, 2, 64), (7, 64, 1)), "q", 0) == 128  # one token: any stride
-    assert b._token_rows(OnGpu((4, 1, 64), (512, 3, 1)), "q", 0) == 512
-    for s in ((512, 64, 2), (512, 128, 1), (64, 64, 1), (0, 64, 1)):
-        with pytest.raises(ValueError):
-            b._token_rows(OnGpu((4, 2, 64), s), "q", 0)
-    with pytest.raises(ValueError, match="CUDA"):
-        b._token_rows(t(4, 2, 64), "q", 0)
-
-
-def test_empty_calls_check_their_tensors():
-    q = torch.empty(2, 0, 4, 64, dtype=BF)
-    with pytest.raises(ValueError, match="CUDA"):
-        b.swa_forward_scored(q, q, q)
+        b.swa_decode_shared(**(shared_args() | bad))
 
 
 # ------------------------------------------------------------------ the reference
