@@ -72,6 +72,46 @@ __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams
   const int warp = threadIdx.x / 32;
   const int t0 = blockIdx.x * kTok;
   const int half = p.rot / 2;
+  const int heads = p.H + 2 * p.Hkv;
+  const int rot_units = p.rot / 16;
+  // What needs no position is on its way before the look-up: the frequency of
+  // this thread's first angle and, in a decoding step (one token a block),
+  // its first two units.
+  const float freq = threadIdx.x < kTok * half ? __ldg(p.inv_freq + threadIdx.x % half) : 0.f;
+  constexpr int kAhead = kTok == 1 ? 2 : 0;
+  struct Unit {
+    int u, hh, tk, c0, c1;
+    bool turn;
+  };
+  auto unit = [&](int i) -> Unit {
+    Unit n;
+    n.u = i % kUnits;
+    n.hh = (i / kUnits) % heads;
+    n.tk = i / (kUnits * heads);
+    n.turn = n.hh < p.H + p.Hkv && n.u < rot_units;
+    // the unit's two vectors: (u, u + rot / 16) in the half form's rotated
+    // part, neighbours everywhere else
+    n.c0 = (!kInter && n.turn) ? n.u : 2 * n.u;
+    n.c1 = (!kInter && n.turn) ? n.u + rot_units : 2 * n.u + 1;
+    return n;
+  };
+  auto source = [&](const Unit& n) -> const uint16_t* {
+    const long long t = t0 + n.tk;
+    if (n.hh < p.H) return p.q + t * p.q_stride + (long long)n.hh * D;
+    if (n.hh < p.H + p.Hkv) return p.k + t * p.k_stride + (long long)(n.hh - p.H) * D;
+    return p.v + t * p.v_stride + (long long)(n.hh - p.H - p.Hkv) * D;
+  };
+  uint4 va[kAhead + 1], vb[kAhead + 1];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = threadIdx.x + k * kThreadsP;
+    if (i < heads * kUnits) {
+      const Unit n = unit(i);
+      const uint16_t* src = source(n);
+      va[k] = *reinterpret_cast<const uint4*>(src + n.c0 * 8);
+      vb[k] = *reinterpret_cast<const uint4*>(src + n.c1 * 8);
+    }
+  }
   if (warp < kTok) {
     const int t = t0 + warp;
     long long pos = -1, row = -1;
@@ -99,48 +139,24 @@ __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams
   __syncthreads();
   for (int i = threadIdx.x; i < kTok * half; i += kThreadsP) {
     const int tk = i / half, f = i % half;
-    const double turns = (double)pos_s[tk] * (double)__ldg(p.inv_freq + f) * 0.15915494309189535;
+    const float w = i == (int)threadIdx.x ? freq : __ldg(p.inv_freq + f);
+    const double turns = (double)pos_s[tk] * (double)w * 0.15915494309189535;
     float sn, cn;
     sincospif(2.f * (float)(turns - rint(turns)), &sn, &cn);
     cs[tk][f] = make_float2(cn, sn);
   }
   __syncthreads();
-  const int heads = p.H + 2 * p.Hkv;
-  const int rot_units = p.rot / 16;
-  for (int i = threadIdx.x; i < kTok * heads * kUnits; i += kThreadsP) {
-    const int u = i % kUnits;
-    const int hh = (i / kUnits) % heads;
-    const int tk = i / (kUnits * heads);
-    const int t = t0 + tk;
-    if (pos_s[tk] < 0) continue;
-    const long long row = row_s[tk];
-    const uint16_t* src;
-    uint16_t* dst;
-    const bool value = hh >= p.H + p.Hkv;
-    if (hh < p.H) {
-      src = p.q + t * p.q_stride + (long long)hh * D;
-      dst = p.q_out + t * p.qo_stride + (long long)hh * D;
-    } else {
-      if (row < 0) continue;
-      const int h = value ? hh - p.H - p.Hkv : hh - p.H;
-      src = (value ? p.v + t * p.v_stride : p.k + t * p.k_stride) + (long long)h * D;
-      dst = (value ? p.v_pages : p.k_pages) + (row * p.Hkv + h) * D;
-    }
-    const bool turn = !value && u < rot_units;
-    // the unit's two vectors: (u, u + rot / 16) in the half form's rotated
-    // part, neighbours everywhere else
-    const int c0 = (!kInter && turn) ? u : 2 * u;
-    const int c1 = (!kInter && turn) ? u + rot_units : 2 * u + 1;
-    const uint4 a = *reinterpret_cast<const uint4*>(src + c0 * 8);
-    const uint4 b = *reinterpret_cast<const uint4*>(src + c1 * 8);
+  auto turn_and_store = [&](const Unit& n, const uint4& a, const uint4& b) {
+    const long long row = row_s[n.tk];
+    if (n.hh >= p.H && row < 0) return;
     uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    if (turn) {
-      const float4* c4 = reinterpret_cast<const float4*>(&cs[tk][8 * u]);
+    if (n.turn) {
+      const float4* c4 = reinterpret_cast<const float4*>(&cs[n.tk][8 * n.u]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 w = c4[e];  // cos, sin of angles 2e and 2e + 1
         if (kInter) {
-          // word e of the eight: elements (2e, 2e + 1) turn by angle e
+          // words 2e and 2e + 1 of the eight turn by those angles
           uint32_t* z = e < 2 ? x + 2 * e : y + 2 * (e - 2);
           const float l0 = lo16(z[0]), h0 = hi16(z[0]), l1 = lo16(z[1]), h1 = hi16(z[1]);
           z[0] = pack_bf16x2(l0 * w.x - h0 * w.y, h0 * w.x + l0 * w.y);
@@ -152,8 +168,27 @@ __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams
         }
       }
     }
-    *reinterpret_cast<uint4*>(dst + c0 * 8) = make_uint4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint4*>(dst + c1 * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+    uint16_t* dst =
+        n.hh < p.H
+            ? p.q_out + (t0 + n.tk) * p.qo_stride + (long long)n.hh * D
+            : (n.hh < p.H + p.Hkv ? p.k_pages + (row * p.Hkv + n.hh - p.H) * D
+                                  : p.v_pages + (row * p.Hkv + n.hh - p.H - p.Hkv) * D);
+    *reinterpret_cast<uint4*>(dst + n.c0 * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(dst + n.c1 * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+  };
+  const int total = kTok * heads * kUnits;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = threadIdx.x + k * kThreadsP;
+    if (i < total && pos_s[0] >= 0) turn_and_store(unit(i), va[k], vb[k]);
+  }
+  for (int i = threadIdx.x + kAhead * kThreadsP; i < total; i += kThreadsP) {
+    const Unit n = unit(i);
+    if (pos_s[n.tk] < 0) continue;
+    const uint16_t* src = source(n);
+    const uint4 a = *reinterpret_cast<const uint4*>(src + n.c0 * 8);
+    const uint4 b = *reinterpret_cast<const uint4*>(src + n.c1 * 8);
+    turn_and_store(n, a, b);
   }
 }
 
