@@ -62,8 +62,8 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
 }
 
 // D: head size; kInter: rotated pairs are adjacent elements; kTok: tokens of
-// a block.
-template <int D, bool kInter, int kTok>
+// a block; kU: units (pairs of vectors) a thread has in flight.
+template <int D, bool kInter, int kTok, int kU>
 __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams p) {
   constexpr int kUnits = D / 16;  // pairs of 16-byte vectors per head
   __shared__ __align__(16) float2 cs[kTok][D / 2];  // (read as float4)
@@ -74,43 +74,53 @@ __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams
   const int half = p.rot / 2;
   const int heads = p.H + 2 * p.Hkv;
   const int rot_units = p.rot / 16;
-  // What needs no position is on its way before the look-up: the frequency of
-  // this thread's first angle and, in a decoding step (one token a block),
-  // its first two units.
-  const float freq = threadIdx.x < kTok * half ? __ldg(p.inv_freq + threadIdx.x % half) : 0.f;
-  constexpr int kAhead = kTok == 1 ? 2 : 0;
-  struct Unit {
-    int u, hh, tk, c0, c1;
-    bool turn;
+  const int n_tok = min(kTok, p.T - t0);
+  // This thread's units: vectors u of the heads slot, slot + kSlots, ... of
+  // the block's tokens one after another (no division on the way).
+  constexpr int kSlots = kThreadsP / kUnits;
+  const int u = threadIdx.x % kUnits;
+  const int step_tk = kSlots / heads, step_hh = kSlots % heads;
+  struct At {
+    int tk, hh;
   };
-  auto unit = [&](int i) -> Unit {
-    Unit n;
-    n.u = i % kUnits;
-    n.hh = (i / kUnits) % heads;
-    n.tk = i / (kUnits * heads);
-    n.turn = n.hh < p.H + p.Hkv && n.u < rot_units;
-    // the unit's two vectors: (u, u + rot / 16) in the half form's rotated
-    // part, neighbours everywhere else
-    n.c0 = (!kInter && n.turn) ? n.u : 2 * n.u;
-    n.c1 = (!kInter && n.turn) ? n.u + rot_units : 2 * n.u + 1;
-    return n;
-  };
-  auto source = [&](const Unit& n) -> const uint16_t* {
-    const long long t = t0 + n.tk;
-    if (n.hh < p.H) return p.q + t * p.q_stride + (long long)n.hh * D;
-    if (n.hh < p.H + p.Hkv) return p.k + t * p.k_stride + (long long)(n.hh - p.H) * D;
-    return p.v + t * p.v_stride + (long long)(n.hh - p.H - p.Hkv) * D;
-  };
-  uint4 va[kAhead + 1], vb[kAhead + 1];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int i = threadIdx.x + k * kThreadsP;
-    if (i < heads * kUnits) {
-      const Unit n = unit(i);
-      const uint16_t* src = source(n);
-      va[k] = *reinterpret_cast<const uint4*>(src + n.c0 * 8);
-      vb[k] = *reinterpret_cast<const uint4*>(src + n.c1 * 8);
+  At at{(int)(threadIdx.x / kUnits) / heads, (int)(threadIdx.x / kUnits) % heads};
+  auto next = [&]() -> At {
+    const At r = at;
+    at.tk += step_tk;
+    at.hh += step_hh;
+    if (at.hh >= heads) {
+      at.hh -= heads;
+      ++at.tk;
     }
+    return r;
+  };
+  // a unit's two vectors: (u, u + rot / 16) in the half form's rotated part,
+  // neighbours everywhere else
+  auto turns_at = [&](int hh) { return hh < p.H + p.Hkv && u < rot_units; };
+  auto second = [&](bool turn) { return (!kInter && turn) ? u + rot_units : 2 * u + 1; };
+  auto first = [&](bool turn) { return (!kInter && turn) ? u : 2 * u; };
+  struct Pair {
+    uint4 a, b;
+  };
+  auto load = [&](const At& n) -> Pair {
+    const long long t = t0 + n.tk;
+    const uint16_t* src =
+        n.hh < p.H ? p.q + t * p.q_stride + n.hh * D
+                   : (n.hh < p.H + p.Hkv ? p.k + t * p.k_stride + (n.hh - p.H) * D
+                                         : p.v + t * p.v_stride + (n.hh - p.H - p.Hkv) * D);
+    const bool turn = turns_at(n.hh);
+    return Pair{*reinterpret_cast<const uint4*>(src + first(turn) * 8),
+                *reinterpret_cast<const uint4*>(src + second(turn) * 8)};
+  };
+  // What needs no position is on its way before the look-up: the frequency of
+  // this thread's first angle and its first units.
+  const float freq = threadIdx.x < kTok * half ? __ldg(p.inv_freq + threadIdx.x % half) : 0.f;
+  At n[kU];
+  Pair v[kU];
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    n[k] = next();
+    if (n[k].tk < n_tok) v[k] = load(n[k]);
   }
   if (warp < kTok) {
     const int t = t0 + warp;
@@ -146,49 +156,46 @@ __global__ void __launch_bounds__(kThreadsP) rope_append_kernel(const RopeParams
     cs[tk][f] = make_float2(cn, sn);
   }
   __syncthreads();
-  auto turn_and_store = [&](const Unit& n, const uint4& a, const uint4& b) {
-    const long long row = row_s[n.tk];
-    if (n.hh >= p.H && row < 0) return;
-    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    if (n.turn) {
-      const float4* c4 = reinterpret_cast<const float4*>(&cs[n.tk][8 * n.u]);
+  while (n[0].tk < n_tok) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 w = c4[e];  // cos, sin of angles 2e and 2e + 1
-        if (kInter) {
-          // words 2e and 2e + 1 of the eight turn by those angles
-          uint32_t* z = e < 2 ? x + 2 * e : y + 2 * (e - 2);
-          const float l0 = lo16(z[0]), h0 = hi16(z[0]), l1 = lo16(z[1]), h1 = hi16(z[1]);
-          z[0] = pack_bf16x2(l0 * w.x - h0 * w.y, h0 * w.x + l0 * w.y);
-          z[1] = pack_bf16x2(l1 * w.z - h1 * w.w, h1 * w.z + l1 * w.w);
-        } else {
-          const float xl = lo16(x[e]), xh = hi16(x[e]), yl = lo16(y[e]), yh = hi16(y[e]);
-          x[e] = pack_bf16x2(xl * w.x - yl * w.y, xh * w.z - yh * w.w);
-          y[e] = pack_bf16x2(yl * w.x + xl * w.y, yh * w.z + xh * w.w);
+    for (int k = 0; k < kU; ++k) {
+      const int tk = n[k].tk, hh = n[k].hh;
+      if (tk >= n_tok || pos_s[tk] < 0) continue;
+      const long long row = row_s[tk];
+      if (hh >= p.H && row < 0) continue;
+      const bool turn = turns_at(hh);
+      uint32_t x[4] = {v[k].a.x, v[k].a.y, v[k].a.z, v[k].a.w};
+      uint32_t y[4] = {v[k].b.x, v[k].b.y, v[k].b.z, v[k].b.w};
+      if (turn) {
+        const float4* c4 = reinterpret_cast<const float4*>(&cs[tk][8 * u]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 w = c4[e];  // cos, sin of angles 2e and 2e + 1
+          if (kInter) {
+            // words 2e and 2e + 1 of the eight turn by those angles
+            uint32_t* z = e < 2 ? x + 2 * e : y + 2 * (e - 2);
+            const float l0 = lo16(z[0]), h0 = hi16(z[0]), l1 = lo16(z[1]), h1 = hi16(z[1]);
+            z[0] = pack_bf16x2(l0 * w.x - h0 * w.y, h0 * w.x + l0 * w.y);
+            z[1] = pack_bf16x2(l1 * w.z - h1 * w.w, h1 * w.z + l1 * w.w);
+          } else {
+            const float xl = lo16(x[e]), xh = hi16(x[e]), yl = lo16(y[e]), yh = hi16(y[e]);
+            x[e] = pack_bf16x2(xl * w.x - yl * w.y, xh * w.z - yh * w.w);
+            y[e] = pack_bf16x2(yl * w.x + xl * w.y, yh * w.z + xh * w.w);
+          }
         }
       }
+      uint16_t* dst = hh < p.H ? p.q_out + (t0 + tk) * p.qo_stride + hh * D
+                               : (hh < p.H + p.Hkv ? p.k_pages + (row * p.Hkv + hh - p.H) * D
+                                                   : p.v_pages +
+                                                         (row * p.Hkv + hh - p.H - p.Hkv) * D);
+      *reinterpret_cast<uint4*>(dst + first(turn) * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(dst + second(turn) * 8) = make_uint4(y[0], y[1], y[2], y[3]);
     }
-    uint16_t* dst =
-        n.hh < p.H
-            ? p.q_out + (t0 + n.tk) * p.qo_stride + (long long)n.hh * D
-            : (n.hh < p.H + p.Hkv ? p.k_pages + (row * p.Hkv + n.hh - p.H) * D
-                                  : p.v_pages + (row * p.Hkv + n.hh - p.H - p.Hkv) * D);
-    *reinterpret_cast<uint4*>(dst + n.c0 * 8) = make_uint4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint4*>(dst + n.c1 * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-  };
-  const int total = kTok * heads * kUnits;
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int i = threadIdx.x + k * kThreadsP;
-    if (i < total && pos_s[0] >= 0) turn_and_store(unit(i), va[k], vb[k]);
-  }
-  for (int i = threadIdx.x + kAhead * kThreadsP; i < total; i += kThreadsP) {
-    const Unit n = unit(i);
-    if (pos_s[n.tk] < 0) continue;
-    const uint16_t* src = source(n);
-    const uint4 a = *reinterpret_cast<const uint4*>(src + n.c0 * 8);
-    const uint4 b = *reinterpret_cast<const uint4*>(src + n.c1 * 8);
-    turn_and_store(n, a, b);
+    for (int k = 0; k < kU; ++k) {
+      n[k] = next();
+      if (n[k].tk < n_tok) v[k] = load(n[k]);
+    }
   }
 }
 
@@ -196,9 +203,9 @@ template <int D, bool kInter>
 int launch(const RopeParams& p, cudaStream_t stream) {
   // few tokens: one a block, so that a decoding step spreads over the SMs
   if (p.T <= 1024)
-    rope_append_kernel<D, kInter, 1><<<(unsigned)p.T, kThreadsP, 0, stream>>>(p);
+    rope_append_kernel<D, kInter, 1, 2><<<(unsigned)p.T, kThreadsP, 0, stream>>>(p);
   else
-    rope_append_kernel<D, kInter, 4><<<(unsigned)((p.T + 3) / 4), kThreadsP, 0, stream>>>(p);
+    rope_append_kernel<D, kInter, 4, 1><<<(unsigned)((p.T + 3) / 4), kThreadsP, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
