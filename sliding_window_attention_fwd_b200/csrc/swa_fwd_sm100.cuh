@@ -45,6 +45,20 @@
 //              producer/issuer warpgroup gives registers to the softmax
 //              warpgroups (setmaxnreg), which then run without spills.
 // Per row: out = O / l (bf16), lse = m + ln l (fp32).
+//
+// Two more forms share the roles, the pipeline and the tiles:
+//  * shaped scores over packed documents (kind 3, swa_score.cuh): the key range
+//    of a tile comes from the documents of its rows, and the softmax warps turn
+//    raw products into capped and biased scores before the exponentials.  The
+//    tensor core has to do 4 D operations a pair as before; the cap adds five
+//    operations a score on the FMA pipe, and what bounds the form is the issue
+//    of two softmax warps per sub-partition.  Causal window of 4096 at N =
+//    8192, H 32 / Hkv 8, D = 128: 376 us plain, 437 with a document table, 489
+//    capped at 50, 465 with a distance bias, 538 with both; with all scores
+//    past half the cap 842 (two more MUFU operations each).
+//  * the shared prefix of a decode (kind 4): the rows of an item are every
+//    sequence's query vectors of one kv head, the keys the prefix's pages, and
+//    the key walk is split until the SMs are full.
 #pragma once
 
 #include <cuda.h>

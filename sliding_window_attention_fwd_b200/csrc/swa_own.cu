@@ -10,11 +10,16 @@
 // bytes behind them as rows 8-15, which fill columns that nobody reads.
 //
 // Tails are short (a few tiles), so a CTA per tail would spend most of its
-// time filling and draining.  The CTAs stay (one per SM, six 32 KB tiles in
-// flight) and walk the items (part, kv head, sequence) i, i + grid, ...: the
-// loads, the MMAs and the softmax run on across item borders (Q and O^T
-// double buffered), and an item's result is written after the next one's
-// first tile.
+// time filling and draining.  The CTAs stay (two per SM) and walk the items
+// (part, kv head, sequence) i, i + grid, ...: the loads, the MMAs and the
+// softmax run on across item borders (Q and O^T double buffered), and an
+// item's result is written after the next one's first tile.
+//
+// Measured, with 8 kv heads of 128: 128 tails of 100 to 700 keys (210 MB) 54
+// us, 3.9 TB/s (70 with a CTA per item and the ring decode's softmax; one CTA
+// per SM with twice the ring 54); 64 tails of 1 to 256 keys (33 MB) 15 us (23;
+// 18.5).  What is left is the chain of a tile (S^T, vote, exponentials, P^T, PV)
+// and tails of uneven length.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer (and TMEM
 // owner), warps 2-5 softmax (thread r: key r of a tile, dimension r of O^T).
