@@ -119,6 +119,7 @@ T* at_or_null(const at::Tensor* t) {
 struct Stream {
   cudaStream_t raw = nullptr;
   bool own = false;  // not the current one
+  Stream() = default;
   Stream(PyObject* o, c10::DeviceIndex dev) {
     if (o == Py_None) {
       raw = c10::cuda::getCurrentCUDAStream(dev).stream();
@@ -138,21 +139,30 @@ struct Stream {
   }
   // Uninitialised device memory that torch's allocator reuses in the order of
   // this stream.
-  at::Tensor scratch(int64_t n, at::ScalarType dtype, const at::Tensor& ref) const {
+  at::Tensor empty(at::IntArrayRef shape, at::TensorOptions options, c10::DeviceIndex dev) const {
     std::optional<c10::cuda::CUDAStreamGuard> guard;
-    if (own) guard.emplace(c10::cuda::getStreamFromExternal(raw, ref.get_device()));
-    return at::empty({n}, ref.options().dtype(dtype));
+    if (own) guard.emplace(c10::cuda::getStreamFromExternal(raw, dev));
+    return at::empty(shape, options);
+  }
+  at::Tensor scratch(int64_t n, at::ScalarType dtype, const at::Tensor& ref) const {
+    return empty({n}, ref.options().dtype(dtype), ref.get_device());
   }
 };
 
-// Result of a call: the caller's tensor, or a new one.
+// (for tensors that are not on a GPU, which is found out later: none)
+Stream stream_of(PyObject* o, const at::Tensor& q) {
+  return q.is_cuda() ? Stream(o, q.get_device()) : Stream();
+}
+
+// Result of a call: the caller's tensor, or a new one (dense, of the call's
+// stream).
 struct Result {
   PyObject* given;
   at::Tensor made;
   const at::Tensor* t;
-  Result(PyObject* o, const char* name, const at::Tensor& like) : given(o) {
+  Result(PyObject* o, const char* name, const at::Tensor& like, const Stream& st) : given(o) {
     if (o == Py_None) {
-      made = at::empty(like.sizes(), like.options());
+      made = st.empty(like.sizes(), like.options(), like.get_device());
       t = &made;
     } else {
       t = &tensor(o, name);
@@ -244,7 +254,8 @@ struct Scored {
 // scale, stream) -> out
 PyObject* forward_scored(PyObject* const* a) {
   const Scored s(a[0], a[1], a[2], a[7], a[8], a[9], a[10]);
-  const Result out(a[3], "out", s.q);
+  const Stream st = stream_of(a[12], s.q);
+  const Result out(a[3], "out", s.q, st);
   need(*out.t, "out", at::kBFloat16, s.q.sizes());
   const at::Tensor* lse = maybe(a[4], "lse");
   if (lse) s.need_lse(*lse);
@@ -254,7 +265,6 @@ PyObject* forward_scored(PyObject* const* a) {
   const int left = int32(a[5], "win_left"), right = int32(a[6], "win_right");
   const float scale = real(a[11]);
   if (!s.empty()) {
-    const Stream st(a[12], s.q.get_device());
     run(s.q.get_device(), "swa_forward_scored", [&] {
       return g_forward(s.q.data_ptr(), s.k.data_ptr(), s.v.data_ptr(), out.t->data_ptr(),
                        at_or_null<float>(lse), s.B, s.H, s.Hkv, s.N, s.D, left, right, &s.score,
@@ -271,7 +281,8 @@ PyObject* backward_scored(PyObject* const* a) {
   const Scored s(a[0], a[1], a[2], a[8], a[9], a[10], a[11]);
   const at::Tensor &out = tensor(a[3], "out"), &dout = tensor(a[4], "dout"),
                    &lse = tensor(a[5], "lse");
-  const Result dq(a[13], "dq", s.q), dk(a[14], "dk", s.k), dv(a[15], "dv", s.v);
+  const Stream st = stream_of(a[16], s.q);
+  const Result dq(a[13], "dq", s.q, st), dk(a[14], "dk", s.k, st), dv(a[15], "dv", s.v, st);
   const struct {
     const at::Tensor& t;
     const char* name;
@@ -286,7 +297,6 @@ PyObject* backward_scored(PyObject* const* a) {
   const int left = int32(a[6], "win_left"), right = int32(a[7], "win_right");
   const float scale = real(a[12]);
   if (!s.empty()) {
-    const Stream st(a[16], s.q.get_device());
     const at::Tensor delta = st.scratch((int64_t)s.B * s.H * s.N, at::kFloat, s.q);
     run(s.q.get_device(), "swa_backward_scored", [&] {
       return g_backward(s.q.data_ptr(), s.k.data_ptr(), s.v.data_ptr(), out.data_ptr(),
@@ -339,7 +349,8 @@ PyObject* rope_append_paged(PyObject* const* a) {
   const int64_t B = table.size(0);
   need(cu, "cu", at::kInt, {B + 1});
   need(pos0, "pos0", at::kLong, {B});
-  const Result out(a[10], "q_out", q);
+  const Stream st = stream_of(a[12], q);
+  const Result out(a[10], "q_out", q, st);
   need(*out.t, "q_out", at::kBFloat16, {T, H, D});
   const int64_t sq = token_rows(q, "q", q), sk = token_rows(k, "k", q), sv = token_rows(v, "v", q),
                 so = token_rows(*out.t, "q_out", q);
@@ -356,7 +367,6 @@ PyObject* rope_append_paged(PyObject* const* a) {
             columns = size32(table.size(1), "block_table"),
             rot = size32(2 * inv.size(0), "inv_freq");
   if (T > 0 && B > 0) {
-    const Stream st(a[12], q.get_device());
     run(q.get_device(), "swa_rope_append_paged", [&] {
       return g_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv,
                     static_cast<const float*>(inv.data_ptr()), rot, inter,
@@ -387,7 +397,8 @@ PyObject* decode_shared(PyObject* const* a) {
   need(pos, "pos", at::kLong, {B});
   if (n_prefix < 0 || ptab.size(0) * page_size < n_prefix)
     bad("prefix_table: expected the pages of n_prefix >= 0 positions");
-  const Result out(a[9], "out", q);
+  const Stream st = stream_of(a[16], q);
+  const Result out(a[9], "out", q, st);
   need(*out.t, "out", at::kBFloat16, {B, H, D});
   const at::Tensor *lse = maybe(a[10], "lse"), *slopes = maybe(a[14], "slopes");
   if (lse) need(*lse, "lse", at::kFloat, {B, H});
@@ -411,7 +422,6 @@ PyObject* decode_shared(PyObject* const* a) {
             columns = size32(table.size(1), "block_table");
   if (B > 0) {
     const auto dev = q.get_device();
-    const Stream st(a[16], dev);
     size_t bytes;
     {
       const c10::cuda::CUDAGuard guard(dev);

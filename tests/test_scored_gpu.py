@@ -265,3 +265,54 @@ def test_two_calls_at_once(swa):
         for g in got[i]:
             for a, b in zip(g, want[i]):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+def test_nan_of_a_seen_key_stays_visible_and_where_it_is(swa, cap, bias):
+    """A NaN key makes the rows that see it NaN, and no others."""
+    q, k, v, _ = inputs(1, 300, 4, 2, 128)
+    cu = torch.tensor([[0, 120, 290]], dtype=torch.int32, device="cuda")
+    kw = {"win_left": 50, "win_right": 0, "softcap": cap, "slopes": slopes_of(4) if bias else None,
+          "cu_docs": cu}
+    want = swa.swa_forward_scored(q, k, v, **kw)
+    k[0, 100, 1, 5] = float("nan")
+    lse = torch.empty(1, 4, 300, device="cuda")
+    got = swa.swa_forward_scored(q, k, v, lse=lse, **kw)
+    sees = torch.zeros(300, dtype=torch.bool)
+    sees[100:120] = True  # (the next document begins at 120)
+    assert torch.isnan(got[0, sees, 2:]).all() and torch.isnan(lse[0, 2:, sees]).all()
+    assert torch.equal(got[0, ~sees], want[0, ~sees])
+    assert torch.equal(got[:, :, :2], want[:, :, :2])
+
+
+def test_unbounded_windows_of_plain_scores(swa):
+    q, k, v, do = inputs(1, 300, 4, 2, 128)
+    lse = [torch.empty(1, 4, 300, device="cuda") for _ in range(2)]
+    res = []
+    for i, (a, b) in enumerate(((-1, -1), (2 ** 31 - 1, 2 ** 31 - 1))):
+        out = swa.swa_forward_scored(q, k, v, lse=lse[i], win_left=a, win_right=b)
+        res.append((out, *swa.swa_backward_scored(q, k, v, out, do, lse[i], win_left=a,
+                                                  win_right=b)))
+    ref = R.forward(q, k, v, -1, -1, 0.0, None, None, None, 0.0, do)
+    for i, r in enumerate(res):
+        R.check({"lse": lse[i], **dict(zip(("out", "dq", "dk", "dv"), r))}, ref,
+                ("out", "lse", "dq", "dk", "dv"))
+
+
+def test_results_belong_to_the_stream_of_the_call(swa):
+    """Memory that another stream's work may still use is not taken for results."""
+    q, k, v, do = inputs(1, 2048, 8, 2, 128)
+    lse = torch.empty(1, 8, 2048, device="cuda")
+    want = swa.swa_forward_scored(q, k, v, win_left=64, win_right=0, softcap=20.0, lse=lse)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = torch.empty_like(q)
+    at = held.data_ptr()
+    del held
+    out = swa.swa_forward_scored(q, k, v, win_left=64, win_right=0, softcap=20.0, stream=side)
+    grads = swa.swa_backward_scored(q, k, v, want, do, lse, win_left=64, win_right=0, softcap=20.0,
+                                    stream=side)
+    assert at not in [t.data_ptr() for t in (out, *grads)]
+    assert torch.empty_like(q).data_ptr() == at  # (it was free)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
