@@ -487,7 +487,8 @@ SWA_API int swa_backward_scored(const void* q, const void* k, const void* v, con
  * device memory, 16-byte aligned, overwritten; two calls may run at the same
  * time if theirs differ.  Nothing is allocated.  D in {64, 128}; H / Hkv <= 8;
  * page_size a multiple of 64; num_pages * page_size < 2^31.  Rows of the pool
- * that the query does not see may hold anything.
+ * that no query sees may hold anything, NaN included, but for V between two
+ * prefix positions that some queries see.
  */
 SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_pages, void* out,
                               float* lse, const int32_t* prefix_table, int n_prefix,

@@ -1084,9 +1084,10 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
                        float scale, cudaStream_t stream, const ScoreArgs* sc = nullptr) {
   using C = BCfg<D>;
   static std::atomic<unsigned long long> attr_dq{0}, attr_dkdv{0};
-  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D, kShaped, SC>), C::kAlloc, attr_dq) ||
-      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D, kShaped, SC>), C::kAlloc,
-                      attr_dkdv))
+  if (!smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dq_kernel<D, kShaped, SC>), C::kAlloc,
+                      attr_dq) ||
+      !smem_attr_once(reinterpret_cast<const void*>(swa_bwd_dkdv_kernel<D, kShaped, SC>),
+                      C::kAlloc, attr_dkdv))
     return SWA_ERR_CUDA;
   int* err = device_error_word();
   if (!err) return SWA_ERR_CUDA;
@@ -1170,8 +1171,9 @@ int launch_bwd_tc_impl(const void* q, const void* k, const void* v, const void* 
         const long grid = ntiles * B * Hkv;
         if (grid <= 0) continue;
         if (grid > 0x7fffffffL) return SWA_ERR_UNSUPPORTED;
-        // (4096 packed tokens with 8 kv heads, 256 CTAs: 161 us in tile order)
-        // and when some walk may be long
+        // Longest walks first where there are more CTAs than SMs and some walk
+        // may be long (4096 packed tokens with 8 kv heads, 256 CTAs: 161 us in
+        // tile order, 148 sorted).
         const long longest =
             L < 0 || R < 0 ? ntiles : std::min(ntiles, ((long)L + R) / kTileM + 2);
         p.sort = kShaped && p.cu_docs && p.n_docs <= 31 && ntiles <= 32 && grid > sm_count() &&
@@ -1202,11 +1204,11 @@ int launch_backward_tc(const void* q, const void* k, const void* v, const void* 
                        float* delta, int B, int H, int Hkv, int N, int D, int L, int R, int d,
                        int bs, float scale, cudaStream_t stream) {
   if (D == 128)
-    return launch_bwd_tc_impl<128, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L,
-                                   R, d, bs, scale, stream);
+    return launch_bwd_tc_impl<128, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H,
+                                             Hkv, N, L, R, d, bs, scale, stream);
   if (D == 64)
-    return launch_bwd_tc_impl<64, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, L, R,
-                                  d, bs, scale, stream);
+    return launch_bwd_tc_impl<64, false, 0>(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H,
+                                            Hkv, N, L, R, d, bs, scale, stream);
   return SWA_ERR_UNSUPPORTED;
 }
 

@@ -472,6 +472,8 @@ SWA_API int swa_forward_scored(const void* q, const void* k, const void* v, void
   st = check_score(score);
   if (st != SWA_OK) return st;
   if (B == 0 || N == 0) return SWA_OK;
+  win_left = win_left < N ? win_left : N;  // (so that positions stay 32-bit)
+  win_right = win_right < N ? win_right : N;
   return launch_fwd_scored(q, k, v, out, lse, B, H, Hkv, N, D, win_left, win_right,
                            score_args(score), resolve_scale(scale, D),
                            static_cast<cudaStream_t>(stream));
@@ -492,15 +494,22 @@ SWA_API int swa_backward_scored(const void* q, const void* k, const void* v, con
   st = check_score(score);
   if (st != SWA_OK) return st;
   if (B == 0 || N == 0) return SWA_OK;
+  win_left = win_left < N ? win_left : N;
+  win_right = win_right < N ? win_right : N;
   return launch_bwd_scored(q, k, v, out, dout, lse, dq, dk, dv, delta, B, H, Hkv, N, D, win_left,
                            win_right, score_args(score), resolve_scale(scale, D),
                            static_cast<cudaStream_t>(stream));
 }
 
+static bool shared_supported(int B, int H, int Hkv, int D, int n_prefix) {
+  return (D == 64 || D == 128) && H / Hkv <= 8 && (int64_t)B * H <= 0x7fffffffLL - 2 * kTileM &&
+         n_prefix <= 0x7fffffff - 2 * kTileN;
+}
+
 SWA_API size_t swa_decode_shared_workspace_bytes(int B, int H, int Hkv, int D, int n_prefix,
                                                  int W, int max_tail) {
-  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || D <= 0 || n_prefix < 0 || W <= 0 ||
-      max_tail < 0)
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || n_prefix < 0 || W <= 0 || max_tail < 0 ||
+      !shared_supported(B, H, Hkv, D, n_prefix))
     return 0;
   return shared_plan(B, H, Hkv, D, n_prefix, W, max_tail).bytes;
 }
@@ -525,11 +534,9 @@ SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_
       (reinterpret_cast<uintptr_t>(prefix_table) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
     return SWA_ERR_ALIGN;
-  if (D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
   // (rows of the pool are 32-bit coordinates of a TMA box)
-  if (H / Hkv > 8 || page_size % kBlockRows != 0 ||
-      (int64_t)num_pages * page_size > 0x7fffffffLL ||
-      (int64_t)B * H > 0x7fffffffLL - 2 * kTileM || n_prefix > 0x7fffffff - 2 * kTileN)
+  if (!shared_supported(B, H, Hkv, D, n_prefix) || page_size % kBlockRows != 0 ||
+      (int64_t)num_pages * page_size > 0x7fffffffLL)
     return SWA_ERR_UNSUPPORTED;
   if (B == 0) return SWA_OK;
   const SharedPlan pl = shared_plan(B, H, Hkv, D, n_prefix, W, max_tail);

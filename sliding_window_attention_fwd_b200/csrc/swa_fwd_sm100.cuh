@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   const int qm1 = q0 + min(qt * kTileM + kTileM - 1, Mq - 1);
   TileRange tr;
   DocTiles dt{};
+  int seen_lo = 0, seen_hi = 0;  // shared prefix: the keys [lo, hi) that rows of the item see
   const DocMask dm{docs && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
                    docs && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
                    p.N, p.L, p.R};
@@ -353,6 +354,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
+    seen_lo = lo;
+    seen_hi = hi + 1;
     tr.kv_begin = lo / kTileN;
     tr.kv_end = hi >= lo ? hi / kTileN + 1 : tr.kv_begin;
     const int n = tr.kv_end - tr.kv_begin;
@@ -1122,8 +1125,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
                         (inplace && t_kv * kTileN < gap_hi && t_kv * kTileN + kTileN > gap_lo);
 
       if (scored) {
-        // padding rows, and pool rows past the prefix, may hold anything
-        const int z0 = docs ? dt.c0 : 0, z1 = docs ? dt.cn : p.N;
+        // padding rows, and pool rows that no query sees, may hold anything
+        const int z0 = docs ? dt.c0 : seen_lo, z1 = docs ? dt.cn : seen_hi;
         if (t_kv * kTileN < z0 || t_kv * kTileN + kTileN > z1) {
           if (!__all_sync(0xffffffffu, clear_v_rows(it, z0, z1))) { ok = false; break; }
         }

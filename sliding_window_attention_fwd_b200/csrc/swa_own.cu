@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
           const float l = red_l[n] + red_l[kNQ + n] + red_l[2 * kNQ + n] + red_l[3 * kNQ + n];
           if (D == 128 || r < D)
             p.part_o[(row_last + n) * D + r] =
-                l > 0.f ? __fdividef(__uint_as_float(ov[n]), l) : 0.f;
+                l == 0.f ? 0.f : __fdividef(__uint_as_float(ov[n]), l);
           if (r == 0)
             p.part_lse[row_last + n] = (m_last[n] + __log2f(l)) * 0.69314718055994531f;
         }

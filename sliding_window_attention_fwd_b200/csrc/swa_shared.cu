@@ -21,6 +21,13 @@
 namespace swa {
 namespace {
 
+// (a NaN among a part's scores makes the row NaN, as in one softmax over all keys)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // One warp per row (sequence, head): the parts' weights e^(lse_i - lse), 32 at
 // a time, one per lane, then the weighted sum of the parts, eight loads in
 // flight per lane.
@@ -35,12 +42,12 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x % 32;
   if (row >= rows) return;
   float m = -INFINITY;
-  for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_lse[(long long)i * rows + row]);
+  for (int i = lane; i < parts; i += 32) m = max_nan(m, part_lse[(long long)i * rows + row]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   float acc[kPer] = {};
   float wsum = 0.f;
-  for (int i0 = 0; i0 < parts && m > -INFINITY; i0 += 32) {
+  for (int i0 = 0; i0 < parts && m != -INFINITY; i0 += 32) {
     const float w = i0 + lane < parts
                         ? __expf(part_lse[(long long)(i0 + lane) * rows + row] - m)
                         : 0.f;
@@ -55,13 +62,13 @@ __global__ void __launch_bounds__(256)
         if (b0 + i >= n) wi[i] = 0.f;
         // (a part without keys of the row has weight 0, and its O may be
         // anything)
-        if (wi[i] > 0.f)
+        if (wi[i] != 0.f)
           o[i] = reinterpret_cast<const Vec*>(part_o + ((long long)(i0 + b0 + i) * rows + row) *
                                                            D)[lane];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (!(wi[i] > 0.f)) continue;
+        if (wi[i] == 0.f) continue;
         const float* f = reinterpret_cast<const float*>(&o[i]);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] += wi[i] * f[e];
@@ -70,14 +77,14 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint16_t* dst = out + row * D + lane * kPer;
   if constexpr (kPer == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lse && lane == 0) lse[row] = wsum > 0.f ? m + __logf(wsum) : -INFINITY;
+  if (lse && lane == 0) lse[row] = wsum == 0.f ? -INFINITY : m + __logf(wsum);
 }
 
 int merge(const float* part_o, const float* part_lse, void* out, float* lse, int parts, int rows,
@@ -126,6 +133,7 @@ SharedPlan shared_plan(int B, int H, int Hkv, int D, int n_prefix, int W, int ma
   const long long rows = (long long)B * (H / Hkv);
   const long long tiles = ((long long)n_prefix + kTileN - 1) / kTileN;
   auto parts_of = [&](int per_item, int per_sm) -> long long {
+    if (tiles == 0) return 0;
     const long long items = (rows + per_item - 1) / per_item * Hkv;
     const long long parts = sms * per_sm / items;
     return parts < 1 ? 1 : (parts < tiles ? parts : tiles);

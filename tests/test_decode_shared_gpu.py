@@ -181,6 +181,59 @@ def test_large_offsets(swa):
     assert torch.equal(got, want)
 
 
+def test_nan_of_a_seen_key_stays_visible_and_where_it_is(swa):
+    """A NaN score makes its row NaN, whichever part holds it, and no other row."""
+    P, page, H, Hkv = 300, 64, 8, 2
+    q, kp, vp, ptab, table, pos = build(P, [P + 400, P + 9, P + 130], H, Hkv, 128, page, seed=5)
+    args = (ptab.cuda(), P, table.cuda(), pos.cuda(), page, 1000)
+    want = swa.swa_decode_shared(q, kp, vp, *args)
+    j = P + 200  # a key of sequence 0 alone
+    own = kp.clone()
+    own[int(table[0, j // page]) * page + j % page, 1, 3] = float("nan")
+    got = swa.swa_decode_shared(q, own, vp, *args)
+    assert torch.isnan(got[0, 4:]).all()
+    assert torch.equal(got[0, :4], want[0, :4]) and torch.equal(got[1:], want[1:])
+    first = kp.clone()
+    first[int(ptab[1]) * page + 7, 0, 3] = float("nan")
+    got = swa.swa_decode_shared(q, first, vp, *args)
+    assert torch.isnan(got[:, :4]).all() and torch.equal(got[:, 4:], want[:, 4:])
+    bad = q.clone()
+    bad[1, 2, 0] = float("nan")
+    lse = torch.empty(3, H, device="cuda")
+    got = swa.swa_decode_shared(bad, kp, vp, *args, lse=lse)
+    assert torch.isnan(got[1, 2]).all() and torch.isnan(lse[1, 2])
+    keep = torch.ones(3, H, dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefix_rows_that_no_query_sees_may_hold_nan(swa, D):
+    """In front of every window, and behind every position inside the prefix."""
+    P, page, W, pos = 500, 64, 90, [333, 350, 401]
+    q, kp, vp, ptab, table, ps = build(P, pos, 8, 2, D, page, seed=6)
+    args = (ptab.cuda(), P, table.cuda(), ps.cuda(), page, W)
+    want = swa.swa_decode_shared(q, kp, vp, *args, keep_prefix=False)
+    for j in [*range(0, 333 - W + 1), *range(402, P)]:
+        row = int(ptab[j // page]) * page + j % page
+        kp[row] = vp[row] = float("nan")
+    assert torch.equal(swa.swa_decode_shared(q, kp, vp, *args, keep_prefix=False), want)
+
+
+def test_many_rows_without_a_prefix(swa):
+    """More rows than the SMs take at once, no prefix and no prefix pages."""
+    B, H, Hkv, page = 1200, 64, 8, 64
+    q, kp, vp, ptab, table, pos = build(0, [b % 5 for b in range(B)], H, Hkv, 64, page, seed=7)
+    got = swa.swa_decode_shared(q, kp, vp, ptab.cuda(), 0, table.cuda(), pos.cuda(), page, 8)
+    some = list(range(0, B, 173))
+    ref = reference(q[some], kp, vp, ptab, table[some], pos[some], 0, page, 8, True, 0.0, None)
+    R.check({"out": got[some]}, ref, ("out",))
+    for b in range(20, B, 5):  # (every fifth sequence has one key: its value)
+        row = int(table[b, 0]) * page
+        if int(pos[b]) == 0:
+            assert torch.equal(got[b], vp[row].repeat_interleave(H // Hkv, 0))
+
+
 def test_captured_and_at_once(swa):
     """Two captured decodes of different sizes replayed in turn; two calls at once."""
     sides, st = [], [torch.cuda.Stream() for _ in range(2)]

@@ -105,7 +105,10 @@ def test_shared_refusals(kw, code):
 def test_shared_workspace_grows_with_the_call():
     f = swa.swa_decode_shared_workspace_bytes
     assert f(0, 8, 2, 128, 100, 64, 5) == 0 and f(2, 9, 2, 128, 100, 64, 5) == 0
+    assert f(2, 8, 2, 96, 100, 64, 5) == 0 and f(2, 18, 2, 128, 100, 64, 5) == 0
     one = f(1, 8, 2, 128, 100, 64, 5)
+    # without a prefix no part of it, however many rows there are
+    assert f(9999, 64, 8, 64, 0, 64, 5) == 9999 * 64 * 65 * 4
     assert one >= 2 * 8 * 129 * 4  # a prefix part and an own part
     assert f(1, 8, 2, 128, 0, 64, 5) >= 8 * 129 * 4
     for tail in (0, 1, 10 ** 4, 2 ** 31 - 1):
