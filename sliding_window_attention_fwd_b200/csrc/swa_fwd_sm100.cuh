@@ -83,6 +83,11 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // of the shaped forms, whose rows begin against 0 (P <= 2^32 is as good in bf16
 // and fp32)
 constexpr float kRescaleShaped = 32.0f;
+// Scores that a cap holds within this many log2 units of 0 (a cap of 50 is 72.1)
+// need no running maximum: every exponential is taken against 0, and P, l and O
+// stay far inside fp32 (and P in bf16, which has its exponents).  Larger caps take
+// the form with a bias, its slopes zero.
+constexpr float kFixedRef = 73.0f;
 struct FwdParams {
   CUtensorMap tmQ[kMaxClasses];
   CUtensorMap tmK[kMaxClasses];
@@ -830,7 +835,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
                             : (block_mode ? (i_phys / p.bs + (p.R / p.bs) * p.d + 1) * p.bs - 1
                                           : i_phys + p.R * p.d);
     constexpr bool cap_on = (SC & 1) != 0, bias_on = (SC & 2) != 0;
-    const float nslope2 = bias_on ? -__ldg(p.slopes + h) * 1.4426950408889634f : 0.f;
+    constexpr bool fixed_ref = SC == 1;
+    const float nslope2 = bias_on && p.slopes ? -__ldg(p.slopes + h) * 1.4426950408889634f : 0.f;
     const float sl2 = p.scale_log2;
     float m_used = -INFINITY;  // running max, scaled log2 units
     float l = 0.f;
@@ -1133,8 +1139,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       }
 
       // adopt a larger max seen on the previous tile (rare after the start)
-      const bool pend = m_pend > m_used;
-      if (__any_sync(0xffffffffu, pend)) {
+      const bool pend = !fixed_ref && m_pend > m_used;
+      if (!fixed_ref && __any_sync(0xffffffffu, pend)) {
         if (!rescale_o(it, pend, m_pend)) { ok = false; break; }
       }
 
@@ -1142,7 +1148,39 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
                       make_float2(0.f, 0.f)};
       float sv[64];
 
-      if constexpr (scored) {
+      if constexpr (fixed_ref) {
+        // exponentials against 0: no maximum to find, none to adopt
+#pragma unroll 1
+        for (int late = 0; late < 2; ++late) {
+          const int hf = e ^ late, pcol = 64 * e + 32 * late;
+          const bool w_ok =
+              mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
+          if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
+          tc_fence_after();
+          read_half(hf, sv);
+          if (late) {
+            // these columns now belong to the early half of the next tile
+            tc_fence_before();
+            mbar_arrive(&l_free[slot]);
+          }
+          const HalfShape q = half_shape(it, hf, sv, 0.f);
+          if (q.small && !__any_sync(0xffffffffu, edge)) {
+            exp_shaped(pcol, sv, ls, q, std::true_type());
+          } else {
+            shape_half(q, sv);
+            mask_half(it, hf, edge, sv);
+            exp_shaped(pcol, sv, ls, q, std::false_type());
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          if (!late) mbar_arrive(&pe_full[slot]);
+        }
+        if (!ok) break;
+        const float2 a2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l += a2.x + a2.y;
+        mbar_arrive(&p_full[slot]);
+        continue;
+      } else if constexpr (scored) {
         // The early half, then the late one (one body, so that the loop stays
         // small): scores against the running maximum m_used (0 while the row
         // has no key), P, and the half's maximum.
@@ -1328,6 +1366,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       tc_fence_before();
       mbar_arrive(&p_full[slot]);
     }
+
+    // (any key's P is at least 2^-kFixedRef)
+    if (fixed_ref && l != 0.f) m_used = 0.f;
 
     // split key walk: this CTA's part goes to the partials (fp32 O / l and
     // lse); an empty part contributes nothing (lse = -inf)
@@ -1516,7 +1557,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           }
         }
       }
-      const float lse_v = none ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
+      const float lse_v = none ? -INFINITY
+                               : (m_used + (fixed_ref ? log2f(l) : __log2f(l))) *
+                                     0.69314718055994531f;
       if (row_valid && split)
         p.part_lse[prow] = lse_v;
       else if (row_valid && p.lse)
@@ -1566,6 +1609,11 @@ bool fwd_regs_fit() {
     known.store((long)fa.numRegs * C::kThreads >= need ? 1 : -1, std::memory_order_release);
   }
   return known.load(std::memory_order_acquire) > 0;
+}
+
+// The kernel's SC for these scores (see kFixedRef).
+inline int score_form(const ScoreArgs& sc) {
+  return sc.kind() == 1 && sc.softcap * 1.4426950408889634f > kFixedRef ? 3 : sc.kind();
 }
 
 // Fills in what shapes the scores.

@@ -61,7 +61,7 @@ int launch_prefix(const SharedArgs& a, const SharedPlan& pl, float* part_o, floa
   sc.slopes = a.slopes;
   auto go = [&](auto d, auto ns) -> int {
     constexpr int kD = decltype(d)::value, kS = decltype(ns)::value;
-    switch (sc.kind()) {
+    switch (score_form(sc)) {
       case 0: return launch<kD, kS, 0>(a, nsplit, part_o, part_lse, stream);
       case 1: return launch<kD, kS, 1>(a, nsplit, part_o, part_lse, stream);
       case 2: return launch<kD, kS, 2>(a, nsplit, part_o, part_lse, stream);

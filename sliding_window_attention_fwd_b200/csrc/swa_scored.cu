@@ -52,7 +52,7 @@ int launch_fwd_scored(const void* q, const void* k, const void* v, void* out, fl
                             stream);
   auto go = [&](auto d, auto ns) -> int {
     constexpr int kD = decltype(d)::value, kS = decltype(ns)::value;
-    switch (sc.kind()) {
+    switch (score_form(sc)) {
       case 0: return launch<kD, kS, 0>(q, k, v, out, lse, B, H, Hkv, N, L, R, sc, scale, stream);
       case 1: return launch<kD, kS, 1>(q, k, v, out, lse, B, H, Hkv, N, L, R, sc, scale, stream);
       case 2: return launch<kD, kS, 2>(q, k, v, out, lse, B, H, Hkv, N, L, R, sc, scale, stream);
