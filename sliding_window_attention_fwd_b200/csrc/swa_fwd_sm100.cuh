@@ -956,6 +956,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     // that whatever lies there, NaN included, adds nothing through P = 0
     auto clear_v_rows = [&](int it, int z0, int z1) -> bool {
       const int st = it % kStages;
+      // (With one stage the tile before may not have landed yet: QK(it - 1) says
+      // nothing of V(it - 1), only of V(it - 2), and a parity wait one phase early
+      // would pass.)
+      if (kStages == 1 && it > 0 &&
+          !mbar_wait(&full_v[0], (uint32_t)(it - 1) & 1u, p.err, abort_flag))
+        return false;
       if (!mbar_wait(&full_v[st], (uint32_t)(it / kStages) & 1u, p.err, abort_flag)) return false;
       const int j = kv_tile(it) * kTileN + r;
       if (j < z0 || j >= z1) {
