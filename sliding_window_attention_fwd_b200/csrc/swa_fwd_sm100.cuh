@@ -52,10 +52,11 @@
 //    raw products into capped and biased scores before the exponentials.  The
 //    tensor core has to do 4 D operations a pair as before; the cap adds five
 //    operations a score on the FMA pipe, and what bounds the form is the issue
-//    of two softmax warps per sub-partition.  Causal window of 4096 at N =
-//    8192, H 32 / Hkv 8, D = 128: 376 us plain, 437 with a document table, 489
-//    capped at 50, 465 with a distance bias, 538 with both; with all scores
-//    past half the cap 842 (two more MUFU operations each).
+//    of two softmax warps per sub-partition.  A cap alone bounds the scores, and
+//    the running maximum falls away (kFixedRef).  Causal window of 4096 at N =
+//    8192, H 32 / Hkv 8, D = 128: 375 us plain, 437 with a document table, 436
+//    capped at 50, 463 with a distance bias, 550 with both; with all scores past
+//    half the cap 842 (two more MUFU operations each).
 //  * the shared prefix of a decode (kind 4): the rows of an item are every
 //    sequence's query vectors of one kv head, the keys the prefix's pages, and
 //    the key walk is split until the SMs are full.
@@ -1011,6 +1012,16 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           if (!((keep >> j) & 1ull)) sv[j] = -INFINITY;
       }
     };
+    // Edge tiles, for one warp's rows and one key half: whether some row misses a
+    // key (returned), and whether no row sees any (none: P = 0, no scores to
+    // read).  Of the halves that an edge crosses a quarter is of either kind.
+    auto half_edge = [&](int it, int hf, bool edge, bool& none) -> bool {
+      none = false;
+      if (!__any_sync(0xffffffffu, edge)) return false;
+      const int n0 = kv_tile(it) * kTileN + hf * 64, last = min(khi, Mv - 1);
+      none = !__any_sync(0xffffffffu, klo <= last && klo < n0 + 64 && last >= n0);
+      return __any_sync(0xffffffffu, klo > n0 || last < n0 + 63);
+    };
     auto half_max = [&](const float (&sv)[64]) -> float {
       float t[8];
 #pragma unroll
@@ -1155,27 +1166,35 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       float sv[64];
 
       if constexpr (fixed_ref) {
-        // exponentials against 0: no maximum to find, none to adopt
-#pragma unroll 1
+        // Exponentials against 0: no maximum to find, none to adopt.  (Both halves
+        // unrolled at D = 128: 160 -> 156 us for 8192 packed tokens; at D = 64 a
+        // loop, 138 against 140 us for a window of 700.)
+#pragma unroll (D == 128 ? 2 : 1)
         for (int late = 0; late < 2; ++late) {
           const int hf = e ^ late, pcol = 64 * e + 32 * late;
           const bool w_ok =
               mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
           tc_fence_after();
-          read_half(hf, sv);
+          bool none;
+          const bool h_edge = half_edge(it, hf, edge, none);
+          if (!none) read_half(hf, sv);
           if (late) {
             // these columns now belong to the early half of the next tile
             tc_fence_before();
             mbar_arrive(&l_free[slot]);
           }
-          const HalfShape q = half_shape(it, hf, sv, 0.f);
-          if (q.small && !__any_sync(0xffffffffu, edge)) {
-            exp_shaped(pcol, sv, ls, q, std::true_type());
+          if (none) {
+            zero_p(pcol);
           } else {
-            shape_half(q, sv);
-            mask_half(it, hf, edge, sv);
-            exp_shaped(pcol, sv, ls, q, std::false_type());
+            const HalfShape q = half_shape(it, hf, sv, 0.f);
+            if (q.small && !h_edge) {
+              exp_shaped(pcol, sv, ls, q, std::true_type());
+            } else {
+              shape_half(q, sv);
+              mask_half(it, hf, h_edge, sv);
+              exp_shaped(pcol, sv, ls, q, std::false_type());
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -1198,12 +1217,28 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
               mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
           tc_fence_after();
-          read_half(hf, sv);
+          // (Windows of 700 / 4096, 64-wide heads, bias alone: 160 / 432 us without
+          // the skip of halves that no row sees, 155 / 443 with it; with the cap
+          // besides 186 / 503 and 187 / 563; neither: whole tiles 132 / 360, halves
+          // 138 / 396.)
+          bool none = false, h_edge = false;
+          if (SC == 2) h_edge = half_edge(it, hf, edge, none);
+          if (SC != 2 || !none) read_half(hf, sv);
           if (late) {
             // these columns now belong to the early half of the next tile
             tc_fence_before();
             mbar_arrive(&l_free[slot]);
           }
+          if (SC == 2 && none) {
+            zero_p(pcol);
+            tmem_wait_st();
+            tc_fence_before();
+            if (!late) mbar_arrive(&pe_full[slot]);
+            continue;
+          }
+          // (votes in front of the reads cost the others up to a tenth)
+          if (SC == 0) h_edge = __any_sync(0xffffffffu, edge);
+          if (SC == 3) h_edge = half_edge(it, hf, edge, none);
           const float m_ref = m_used == -INFINITY ? 0.f : m_used;
           const HalfShape q = half_shape(it, hf, sv, m_ref);
           float2 lh[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
@@ -1211,12 +1246,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           // the usual half, with no key to mask: P is formed while the half's
           // maximum is found (a row's first against 0, which holds for any
           // maximum in [-20, 64]); otherwise the maximum comes first
-          const bool usual = !q.diag && q.small && !__any_sync(0xffffffffu, edge);
+          const bool usual = !q.diag && q.small && !h_edge;
           if (usual) {
             exp_shaped(pcol, sv, lh, q, std::true_type());
           } else {
             shape_half(q, sv);
-            mask_half(it, hf, edge, sv);
+            mask_half(it, hf, h_edge, sv);
           }
           const float hmax = half_max(sv);  // above m_ref
           tmax = fmaxf(tmax, m_ref + hmax);
