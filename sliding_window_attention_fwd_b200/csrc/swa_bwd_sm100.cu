@@ -258,6 +258,14 @@ __device__ __forceinline__ void exp_chunk(bool edge, int lo, int hi, float2 (&x)
   }
 }
 
+// Edge tiles, for a warp's 32 rows and a block of 32 columns (lo, hi: the row's
+// columns counted from the block's first): whether some row misses a column, and
+// whether no row has any (P = 0 without a look at the scores).
+__device__ __forceinline__ void block_edge(int lo, int hi, bool& edge, bool& none) {
+  none = !__any_sync(0xffffffffu, lo <= hi && lo < 32 && hi >= 0);
+  edge = __any_sync(0xffffffffu, lo > 0 || hi < 31);
+}
+
 // Zeros over the rows of a 128-row tile outside [z0, z1) (thread r: row r of
 // the tile at row0): padding may hold anything, and a product with P = 0 or
 // dS = 0 would keep its NaN.
@@ -566,18 +574,27 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
       tc_fence_after();
       float2 pr[kCpg][16];
+      bool b_edge[kCpg] = {}, b_none[kCpg] = {};
 #pragma unroll
       for (int i = 0; i < kCpg; ++i) {
         const int ch = cg * kCpg + i;
+        const int n0 = t * kTileN + 32 * ch;
+        if (kShaped && edge) {
+          block_edge(klo - n0, khi - n0, b_edge[i], b_none[i]);
+          if (b_none[i]) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pr[i][e] = make_float2(0.f, 0.f);
+            continue;
+          }
+        }
         uint32_t sv[32];
         tmem_ld32(tS + 32 * ch, sv);
         tmem_wait_ld();
-        const int n0 = t * kTileN + 32 * ch;
         if constexpr (kShaped) {
           float2 x[16], t[16];
           shape_chunk<SC>(p.cap, sl2, nslope2, sv, m_v, n0,
                           [&](int) { return make_float2(-lse2, -lse2); }, x, t);
-          exp_chunk<SC>(edge, klo - n0, khi - n0, x, t, pr[i], [](int, float2) {});
+          exp_chunk<SC>(b_edge[i], klo - n0, khi - n0, x, t, pr[i], [](int, float2) {});
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -617,7 +634,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         uint32_t dpv[32];
         tmem_ld32(tP + 32 * ch, dpv);
         tmem_wait_ld();
-        if (kShaped && edge) {
+        if (kShaped && (b_edge[i] || b_none[i])) {
           // dP of masked places may be NaN (padding): 0 there
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -927,15 +944,28 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       tc_fence_after();
       const float* vl = vec + st * 2 * kTileM;
       float2 pr[kCpg][16];
+      bool b_edge[kCpg] = {}, b_none[kCpg] = {};
 #pragma unroll
       for (int i = 0; i < kCpg; ++i) {
         const int ch = cg * kCpg + i;
-        uint32_t sv[32];
-        tmem_ld32(tS + 32 * ch, sv);
-        tmem_wait_ld();
         const int i0 = qt * kTileM + 32 * ch;
         const float4* l4 = reinterpret_cast<const float4*>(vl + 32 * ch);
         uint32_t pp[16];
+        if (kShaped && edge) {
+          block_edge(qlo - i0, qhi - i0, b_edge[i], b_none[i]);
+          if (b_none[i]) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              pr[i][e] = make_float2(0.f, 0.f);
+              pp[e] = 0u;
+            }
+            tmem_st16(tS + 32 * kCpg * cg + 16 * i, pp);
+            continue;
+          }
+        }
+        uint32_t sv[32];
+        tmem_ld32(tS + 32 * ch, sv);
+        tmem_wait_ld();
         if constexpr (kShaped) {
           float2 x[16], t[16];
           shape_chunk<SC>(p.cap, sl2, nslope2, sv, j_v, i0,
@@ -944,7 +974,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                             return e & 1 ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y);
                           },
                           x, t);
-          exp_chunk<SC>(edge, qlo - i0, qhi - i0, x, t, pr[i],
+          exp_chunk<SC>(b_edge[i], qlo - i0, qhi - i0, x, t, pr[i],
                         [&](int e, float2 v) { pp[e] = pack_bf16x2(v.x, v.y); });
         } else {
 #pragma unroll
@@ -1002,7 +1032,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         uint32_t dpv[32];
         tmem_ld32(tP + 32 * ch, dpv);
         tmem_wait_ld();
-        if (kShaped && edge) {
+        if (kShaped && (b_edge[i] || b_none[i])) {
           // dP of masked places may be NaN (padding): 0 there
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
