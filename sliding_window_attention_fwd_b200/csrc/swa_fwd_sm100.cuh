@@ -54,9 +54,9 @@
 //    operations a score on the FMA pipe, and what bounds the form is the issue
 //    of two softmax warps per sub-partition.  A cap alone bounds the scores, and
 //    the running maximum falls away (kFixedRef).  Causal window of 4096 at N =
-//    8192, H 32 / Hkv 8, D = 128: 375 us plain, 437 with a document table, 436
-//    capped at 50, 463 with a distance bias, 550 with both; with all scores past
-//    half the cap 842 (two more MUFU operations each).
+//    8192, H 32 / Hkv 8, D = 128: 375 us plain, 432 with a document table, 435
+//    capped at 50, 460 with a distance bias, 550 with both; with all scores past
+//    half the cap 795 (two more MUFU operations each).
 //  * the shared prefix of a decode (kind 4): the rows of an item are every
 //    sequence's query vectors of one kv head, the keys the prefix's pages, and
 //    the key walk is split until the SMs are full.
@@ -175,7 +175,7 @@ struct FwdParams {
   int page_size, num_pages, keep;
 };
 
-template <int D, int NSLOT, int NSTREAM, int KIND>
+template <int D, int NSLOT, int NSTREAM, int KIND, int SC = 0>
 struct Cfg {
   static constexpr int kTile = D / 64 * kChunkBytes;        // 128 rows x D bf16
   static constexpr int kStageBytes = 2 * NSTREAM * kTile;   // K and V of every stream
@@ -198,9 +198,20 @@ struct Cfg {
   // full_q, full_k[S], empty_k[S], full_v[S], empty_v[S],
   // se_full[2], sl_full[2], l_free[2], p_full[2], o_done[2], o_final[2],
   // pe_full[2], oe_done[2], peer_free, xfer
-  static constexpr int kNumBars = 1 + 4 * kStages + 18;
+  // documents, two slots, no bias: one CTA per SM goes from item to item (kind 3 at
+  // D = 128, per item and chained: 8192 tokens in 8 documents 134 and 110-122 us, in 7
+  // ragged ones capped 156 and 150, window of 700 160 and 149; with a bias the loop
+  // gets longer and a window of 4096 463 and 495.  With one slot two CTAs per SM
+  // already overlap, D = 64 capped 133 and 148.)
+  static constexpr bool kChain = KIND == 3 && NSLOT == 2 && SC < 2;
+  // kChain: q_free, o_free[2], done[2], item_full[2], item_free[2], claimed
+  static constexpr int kNumBars = 1 + 4 * kStages + 18 + (kChain ? 10 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kTotal = kMisc + 16;
+  // kChain: the answer to a claim, and two items (kItemInts integers each)
+  static constexpr int kClaim = (kMisc + 16 + 15) / 16 * 16;
+  static constexpr int kItemInts = 16 + 64;
+  static constexpr int kItems = kClaim + 16;
+  static constexpr int kTotal = kChain ? kItems + 2 * kItemInts * 4 : kMisc + 16;
   static constexpr int kAlloc = kTotal + 1024;  // slack for 1024-byte alignment
   static_assert(kAlloc <= 232448, "shared memory budget");
   // paired parts: the half of O the other part writes (fp32, NSLOT x 128
@@ -215,10 +226,10 @@ struct Cfg {
 // band with shaped scores and documents; 4 the shared prefix of a decode.
 // SC (kinds 3 and 4): 1 a tanh cap, 2 a distance bias, 3 both.
 template <int D, int NSLOT, int NSTREAM, int KIND, int SC = 0>
-__global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
-                                  Cfg<D, NSLOT, NSTREAM, KIND>::kMinBlocks)
+__global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
+                                  Cfg<D, NSLOT, NSTREAM, KIND, SC>::kMinBlocks)
     swa_fwd_sm100_kernel(const __grid_constant__ FwdParams p) {
-  using C = Cfg<D, NSLOT, NSTREAM, KIND>;
+  using C = Cfg<D, NSLOT, NSTREAM, KIND, SC>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -241,6 +252,15 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   // written); the other part's half of O and (m, l) have landed here
   uint64_t* peer_free = oe_done + 2;
   uint64_t* xfer = peer_free + 1;
+  // kChain: every QK of an item done; its O read out [slot]; every MMA done
+  // [slot]; a further item described / read [item & 1]; the claim answered
+  uint64_t* q_free = xfer + 1;
+  uint64_t* o_free = q_free + 1;
+  uint64_t* mma_done = o_free + 2;
+  uint64_t* item_full = mma_done + 2;
+  uint64_t* item_free = item_full + 2;
+  uint64_t* claimed = item_free + 2;
+  int* items = reinterpret_cast<int*>(smem + C::kItems);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
 
@@ -255,6 +275,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   int x = blockIdx.x;
   constexpr bool glob = KIND == 2;
   constexpr bool docs = KIND == 3;
+  constexpr bool chain = C::kChain;
   constexpr bool shared = KIND == 4;
   constexpr bool scored = docs || shared;
   // the own keys' kernel reads nothing of this one's: it may start with it
@@ -266,11 +287,11 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     sp = x % p.nsplit;
     x /= p.nsplit;
   }
-  const int hp = shared ? 0 : x % npair;
+  int hp = shared ? 0 : x % npair;
   x /= shared ? 1 : npair;
   const int g_kv = shared ? x % p.Hkv : 0;
   x /= shared ? p.Hkv : 1;
-  const int b = shared ? 0 : x % p.B;
+  int b = shared ? 0 : x % p.B;
   x /= shared ? 1 : p.B;
   int cl = 0, qt = 0, gq0 = 0, gcnt = 0;
   const int sr0 = shared ? x * NSLOT * kTileM : 0;  // first query row of this item
@@ -337,9 +358,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   TileRange tr;
   DocTiles dt{};
   int seen_lo = 0, seen_hi = 0;  // shared prefix: the keys [lo, hi) that rows of the item see
-  const DocMask dm{docs && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
-                   docs && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs,
-                   p.N, p.L, p.R};
+  DocMask dm{docs && p.cu_docs ? p.cu_docs + (size_t)b * (p.n_docs + 1) : nullptr,
+             docs && p.doc_pre ? p.doc_pre + (size_t)b * p.n_docs : nullptr, p.n_docs, p.N, p.L,
+             p.R};
   if (docs) {
     dt = doc_tiles<false>(dm, qm0, qm1);
     tr.kv_begin = dt.begin;
@@ -395,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   }
   // in place: the masked rows between the history and the chunk
   const int gap_lo = inplace ? ip_hs + p.win - 1 : 0, gap_hi = inplace ? ip_cs : 0;
-  const int n_band = tr.kv_end - tr.kv_begin;
+  int n_band = tr.kv_end - tr.kv_begin;
   int n_gtiles = (!glob || gitem) ? 0 : (p.n_global + kTileN - 1) / kTileN;
   if (n_gtiles > 0 && p.d == 1 && p.bs <= 1 && p.L >= 0) {
     // token-level band: a global key g joins row i unless i - L <= g <= i +
@@ -412,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     const bool right = p.R > 0 && g_last > qr0 + p.R;  // causal (R == 0) takes none right
     if (!left && !right) n_gtiles = 0;
   }
-  const int n_tiles = n_band + n_gtiles;
+  int n_tiles = n_band + n_gtiles;
   const bool block_mode = p.bs > 1;
   const int map_idx = block_mode ? 0 : cl;
 
@@ -421,6 +442,44 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
   // to near, a steep bias would raise the running maximum on every tile.
   int near = tr.kv_end - 1;
   if (docs && (SC & 2)) near = min(near, max(tr.kv_begin, qt));
+  // kChain: a CTA goes on with items of CTAs that have not started (see the
+  // producer).  Makes item (qt_, hp_, b_) and its walk [begin, end) the current one.
+  auto take_item = [&](int qt_, int hp_, int b_, int begin, int end) {
+    qt = qt_;
+    hp = hp_;
+    b = b_;
+    for (int s = 0; s < NSLOT; ++s) {
+      head[s] = hp * NSLOT + s;
+      kvh[s] = head[s] / grp;
+    }
+    if (p.cu_docs) dm.cu = p.cu_docs + (size_t)b * (p.n_docs + 1);
+    if (p.doc_pre) dm.pre = p.doc_pre + (size_t)b * p.n_docs;
+    tr.kv_begin = begin;
+    tr.kv_end = end;
+    n_tiles = n_band = end - begin;
+    near = end - 1;
+    if (SC & 2) near = min(near, max(begin, qt));
+  };
+  // Waits for the description of item n > 0 and takes it (false: there is none, or
+  // a wait gave up).
+  auto next_item = [&](int n) -> bool {
+    if (!mbar_wait(&item_full[n & 1], (uint32_t)((n - 1) >> 1) & 1u, p.err, abort_flag))
+      return false;
+    const int* d = items + (n & 1) * C::kItemInts;
+    const int at = d[0];
+    if (at >= 0) take_item(at, d[1], d[2], d[3], d[4]);
+    dt.int_lo = d[5];
+    dt.int_hi = d[6];
+    dt.mlo = d[7];
+    dt.mhi = d[8];
+    dt.c0 = d[9];
+    dt.cn = d[10];
+    dt.base = d[11];
+    dt.bound = d[16 + lane];
+    dt.pre = d[48 + lane];
+    mbar_arrive(&item_free[n & 1]);
+    return at >= 0;
+  };
   auto kv_tile = [&](int it) -> int {
     if (!(SC & 2)) return tr.kv_begin + it;
     const int before = near - tr.kv_begin + 1;
@@ -466,8 +525,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
                       &p.tmQ[map_idx], full_q, cc * 64, head[s] + (stack ? hh : 0),
                       stack ? 0 : box_row(qt * kTileM + hh * 64), b);
   };
-  auto load_kv = [&](int it, int kv) {
-    const int st = it % kStages;
+  // (base: tiles of the items before)
+  auto load_kv = [&](int it, int kv, int base = 0) {
+    const int st = (base + it) % kStages;
     uint64_t* ful = kv ? &full_v[st] : &full_k[st];
     uint8_t* dst = smem + C::kRing + st * C::kStageBytes + kv * NSTREAM * C::kTile;
     const int t = kv_tile(it);
@@ -522,6 +582,16 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     }
     mbar_init(peer_free, 128 * NSLOT);
     mbar_init(xfer, 128 * NSLOT);
+    if (chain) {
+      mbar_init(q_free, NSLOT);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&o_free[i], 128);
+        mbar_init(&mma_done[i], 1);
+        mbar_init(&item_full[i], 1);
+        mbar_init(&item_free[i], NSLOT * 129);
+      }
+      mbar_init(claimed, 1);
+    }
     fence_mbar_init();
     // (an empty part of a split key walk loads nothing: no copy may still
     // be landing in shared memory when the CTA exits)
@@ -571,9 +641,104 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     // producer and issuers need few registers: hand the rest to the softmax
     // warpgroups (two slots: 128 x 56 + 256 x 208 = 60416 <= 384 x 168
     // launched; one slot, two CTAs per SM: 128 x 56 + 128 x 200 = 256 x 128)
-    if (NSLOT == 2 || C::kMinBlocks == 2)
+    // (kChain: 128 x 80, its producer looks documents up)
+    if (chain)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+    else if (NSLOT == 2 || C::kMinBlocks == 2)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
-    if (warp == 0) {
+    if (chain && warp == 0) {
+      // ===================== producer (kChain) =====================
+      // The walks of packed documents are short, and a CTA per item would spend a
+      // third of its life starting and ending.  So a CTA claims the next item of
+      // the grid that has not been started while it still works on its own, and
+      // loads, MMAs and softmax run on across the border: the claims go in launch
+      // order, which keeps the balance of the hardware's scheduling.
+      int base = 0, claims = 0, last_k = n_early_k - 1, last_v = -1;
+      int full = n_tiles > 0 ? 1 : 0;  // items whose Q is or was under way (the first's is)
+      bool ok = true;
+      auto all_wait = [&](uint64_t* bar, int phase) {
+        return (bool)__all_sync(0xffffffffu,
+                                mbar_wait(bar, (uint32_t)phase & 1u, p.err, abort_flag));
+      };
+      for (int n = 0; ok; ++n) {
+        for (int it = 0; ok && it < n_tiles; ++it) {
+          const int gt = base + it;
+          for (int kv = 0; ok && kv < 2; ++kv) {  // 0: K, 1: V
+            if (n == 0 && it < (kv ? n_early_v : n_early_k)) continue;
+            uint64_t* emp = kv ? &empty_v[gt % kStages] : &empty_k[gt % kStages];
+            if (gt >= kStages && !all_wait(emp, gt / kStages - 1)) {
+              ok = false;
+              break;
+            }
+            (kv ? last_v : last_k) = gt;
+            if (!withheld(gt, kv) && lane == 0) load_kv(it, kv, base);
+            if (n > 0 && it == 0 && kv == 0) {
+              // Q of the item before has been read by every QK
+              ok = full == 0 || all_wait(q_free, full - 1);
+              if (ok && lane == 0) load_q();
+              if (ok) ++full;
+            }
+          }
+        }
+        if (!ok) break;
+        base += n_tiles;
+        // claimed only now, so that a long walk does not hold a second item
+        if (lane == 0) {
+          mbar_arrive_expect_tx(claimed, 16);
+          claim_next_cta(smem_u32(smem + C::kClaim), claimed);
+        }
+        ++claims;
+        // the answer: another item, or none left
+        if (!all_wait(claimed, n)) break;
+        int y = claimed_cta(smem_u32(smem + C::kClaim));
+        __syncwarp();
+        fence_proxy_async_smem();  // (read, before the next claim writes it)
+        int at = -1;
+        if (y >= 0) {
+          hp = y % npair;
+          y /= npair;
+          b = y % p.B;
+          at = p.qtile_prefix[1] - 1 - y / p.B;
+          take_item(at, hp, b, 0, 0);
+          dt = doc_tiles<false>(dm, at * kTileM, min(at * kTileM + kTileM, p.N) - 1);
+          take_item(at, hp, b, dt.begin, dt.end);
+        }
+        const int m = n + 1;
+        if (m >= 3 && !all_wait(&item_free[m & 1], (m - 3) >> 1)) break;
+        int* d = items + (m & 1) * C::kItemInts;
+        if (lane == 0) {
+          d[0] = at;
+          d[1] = hp;
+          d[2] = b;
+          d[3] = dt.begin;
+          d[4] = dt.end;
+          d[5] = dt.int_lo;
+          d[6] = dt.int_hi;
+          d[7] = dt.mlo;
+          d[8] = dt.mhi;
+          d[9] = dt.c0;
+          d[10] = dt.cn;
+          d[11] = dt.base;
+        }
+        d[16 + lane] = dt.bound;
+        d[48 + lane] = dt.pre;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_full[m & 1]);
+        if (at < 0) break;
+      }
+      if (lane == 0 && *abort_flag) {
+        // leave no copy and no answer writing shared memory behind
+#ifdef SWA_TEST_WITHHOLD_TILE
+        const int skip = SWA_TEST_WITHHOLD_TILE;
+#else
+        const int skip = -1;
+#endif
+        drain_copies(full_q, 1, 0, full - 1);
+        drain_copies(full_k, kStages, 0, last_k, skip);
+        drain_copies(full_v, kStages, 0, last_v);
+        drain_copies(claimed, 1, 0, claims - 1);
+      }
+    } else if (warp == 0) {
       // =========================== producer ===========================
       if (gitem) {
         // gather the tile's global query rows (zeros past the last) with
@@ -674,12 +839,12 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       // half of tile j+1 (same columns) is issued then, while the softmax
       // is still busy with tile j, and only the late half waits for PV(j).
       const int s = warp - 1;
-      if (n_tiles > 0 && slot_ok[s] && lane == 0) {
+      if ((chain || n_tiles > 0) && slot_ok[s] && lane == 0) {
         const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN / 2, 0, 0);
         const uint32_t idesc_pv = idesc_bf16_f32(kTileM, D, 0, 1);
         // Descriptors are built once; every MMA then only adds a compile-time
         // offset (start address field, 16-byte units) to a base descriptor.
-        const uint64_t dq = sdesc_sw128(q_addr, 16, 1024) + (uint64_t)s * (C::kTile >> 4);
+        const uint64_t dq0 = sdesc_sw128(q_addr, 16, 1024) + (uint64_t)s * (C::kTile >> 4);
         const uint64_t dk0 = sdesc_sw128(ring_addr, 16, 1024) +
                              (NSTREAM == 2 ? (uint64_t)s * (C::kTile >> 4) : 0ull);
         const uint64_t dv0 = sdesc_sw128(ring_addr + NSTREAM * C::kTile, kChunkBytes, 1024) +
@@ -689,7 +854,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
         const uint32_t tslot = tmem + 128u * s;
         // S[:, 64 hf : 64 hf + 64] = Q_s K[64 hf : 64 hf + 64]^T of tile it
         auto qk_half = [&](int it, int hf, uint64_t* done) {
-          const uint64_t dk = dk0 + (uint64_t)(it % kStages) * kStageStep + (uint64_t)hf * kHalfRows;
+          const uint64_t dq = chain ? sdesc_fresh(dq0) : dq0;
+          const uint64_t dk = (chain ? sdesc_fresh(dk0) : dk0) +
+                              (uint64_t)(it % kStages) * kStageStep + (uint64_t)hf * kHalfRows;
           const uint32_t ts = tslot + 64u * hf;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -704,8 +871,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
         // The early half's share is issued as soon as its P is written, so
         // after the softmax finishes a tile only a quarter-tile of PV stands
         // between it and the late half of the next tile's S.
-        auto pv_half = [&](int it, bool early) {
-          const uint64_t dv = dv0 + (uint64_t)(it % kStages) * kStageStep;
+        auto pv_half = [&](int it, bool first, bool early) {
+          const uint64_t dv =
+              (chain ? sdesc_fresh(dv0) : dv0) + (uint64_t)(it % kStages) * kStageStep;
           const uint32_t to = tmem + C::kOcol + (uint32_t)D * s;
           const int e = it & 1;
           const uint32_t tp = tslot + 64u * (uint32_t)e + (early ? 0u : 32u);
@@ -714,51 +882,78 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
           for (int kk = 0; kk < 4; ++kk) {
             const int k = kh * 4 + kk;
             mma_ts(to, tp + 8u * kk, dv + (uint64_t)((k * 2048) >> 4), idesc_pv,
-                   (it > 0 || !early || kk > 0) ? 1u : 0u);
+                   (!first || kk > 0) ? 1u : 0u);
           }
         };
-        // (a shared prefix's query rows were in place at the block barrier)
-        bool ok = (shared || mbar_wait(full_q, 0, p.err, abort_flag)) &&
-                  mbar_wait(&full_k[0], 0, p.err, abort_flag);
-        tc_fence_after();
-        if (ok) {
-          qk_half(0, 0, &se_full[s]);
-          qk_half(0, 1, &sl_full[s]);
-          tc_commit(&empty_k[0]);
-        }
-        for (int it = 0; ok && it < n_tiles; ++it) {
-          const int st = it % kStages;
-          const bool more = it + 1 < n_tiles;
-          const int e_next = (it + 1) & 1;  // early half of tile it + 1
-          // the early half's P is in TMEM: its share of PV goes first
-          if (!mbar_wait(&pe_full[s], (uint32_t)it & 1u, p.err, abort_flag)) break;
-          if (!mbar_wait(&full_v[st], (uint32_t)(it / kStages) & 1u, p.err, abort_flag)) break;
-          tc_fence_after();
-          pv_half(it, true);
-          tc_commit(&oe_done[s]);
-          if (more) {
-            // the softmax has read the late half of tile it; K of tile it + 1
-            if (!mbar_wait(&l_free[s], (uint32_t)it & 1u, p.err, abort_flag)) break;
-            if (!mbar_wait(&full_k[(it + 1) % kStages], (uint32_t)((it + 1) / kStages) & 1u,
-                           p.err, abort_flag))
+        // base: tiles of the items before; full: items with tiles so far (kChain)
+        int base = 0, full = 0;
+        int nt = n_tiles;
+        for (int n = 0;; ++n) {
+          if (chain && n > 0) {
+            if (!mbar_wait(&item_full[n & 1], (uint32_t)((n - 1) >> 1) & 1u, p.err, abort_flag))
               break;
-            tc_fence_after();
-            qk_half(it + 1, e_next, &se_full[s]);
+            const int* d = items + (n & 1) * C::kItemInts;
+            const int at = d[0];
+            nt = d[4] - d[3];
+            mbar_arrive(&item_free[n & 1]);
+            if (at < 0) break;
           }
-          // P of tile it is in TMEM; V of tile it
-          if (!mbar_wait(&p_full[s], (uint32_t)it & 1u, p.err, abort_flag)) break;
+          if (chain && nt == 0) continue;
+          // (a shared prefix's query rows were in place at the block barrier)
+          bool ok = (shared || mbar_wait(full_q, (uint32_t)full & 1u, p.err, abort_flag)) &&
+                    mbar_wait(&full_k[base % kStages], (uint32_t)(base / kStages) & 1u, p.err,
+                              abort_flag);
           tc_fence_after();
-          pv_half(it, false);
-          tc_commit(&o_done[s]);
-          tc_commit(&empty_v[st]);
-          if (more) {
-            qk_half(it + 1, e_next ^ 1, &sl_full[s]);
-            tc_commit(&empty_k[(it + 1) % kStages]);
+          if (ok) {
+            qk_half(base, base & 1, &se_full[s]);
+            qk_half(base, (base & 1) ^ 1, &sl_full[s]);
+            tc_commit(&empty_k[base % kStages]);
+            if (chain && nt == 1) tc_commit(q_free);
           }
+          // (O of the item before has been read out)
+          if (chain && ok && full > 0)
+            ok = mbar_wait(&o_free[s], (uint32_t)(full - 1) & 1u, p.err, abort_flag);
+          for (int it = 0; ok && it < nt; ++it) {
+            const int gt = base + it, st = gt % kStages;
+            const bool more = it + 1 < nt;
+            const int e_next = (gt + 1) & 1;  // early half of tile it + 1
+            ok = false;
+            // the early half's P is in TMEM: its share of PV goes first
+            if (!mbar_wait(&pe_full[s], (uint32_t)gt & 1u, p.err, abort_flag)) break;
+            if (!mbar_wait(&full_v[st], (uint32_t)(gt / kStages) & 1u, p.err, abort_flag)) break;
+            tc_fence_after();
+            pv_half(gt, it == 0, true);
+            tc_commit(&oe_done[s]);
+            if (more) {
+              // the softmax has read the late half of tile it; K of tile it + 1
+              if (!mbar_wait(&l_free[s], (uint32_t)gt & 1u, p.err, abort_flag)) break;
+              if (!mbar_wait(&full_k[(gt + 1) % kStages], (uint32_t)((gt + 1) / kStages) & 1u,
+                             p.err, abort_flag))
+                break;
+              tc_fence_after();
+              qk_half(gt + 1, e_next, &se_full[s]);
+            }
+            // P of tile it is in TMEM; V of tile it
+            if (!mbar_wait(&p_full[s], (uint32_t)gt & 1u, p.err, abort_flag)) break;
+            tc_fence_after();
+            pv_half(gt, false, false);
+            tc_commit(&o_done[s]);
+            tc_commit(&empty_v[st]);
+            if (more) {
+              qk_half(gt + 1, e_next ^ 1, &sl_full[s]);
+              tc_commit(&empty_k[(gt + 1) % kStages]);
+              if (chain && it + 2 == nt) tc_commit(q_free);
+            }
+            ok = true;
+          }
+          // o_final completes once every MMA issued above has finished (also on
+          // the abort path, so TMEM is quiescent before it is freed).
+          tc_commit(&o_final[s]);
+          base += nt;
+          ++full;
+          if (!chain || !ok) break;
         }
-        // o_final completes once every MMA issued above has finished (also on
-        // the abort path, so TMEM is quiescent before it is freed).
-        tc_commit(&o_final[s]);
+        if (chain) tc_commit(&mma_done[s]);
       }
       __syncwarp();
     }
@@ -774,6 +969,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     const uint32_t tS = tmem + 128u * slot + lane_off;
     const uint32_t tO = tmem + C::kOcol + (uint32_t)D * slot + lane_off;
     // stacked: lanes 64-127 are the slot's second head, same tokens
+    int base = 0, full = 0, n_item = 0;  // (kChain: as the issuers')
+  another_item:
     const int sR = sr0 + slot * kTileM + r;  // shared prefix: row among the kv head's queries
     const int h = shared ? g_kv * grp + sR % grp : head[slot] + (stack ? (r >> 6) : 0);
     const int m_row = stack ? (r & 63) : qt * kTileM + r;  // local query row
@@ -956,14 +1153,14 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     // zeros over the V rows of tile it outside [z0, z1) (thread r: row r), so
     // that whatever lies there, NaN included, adds nothing through P = 0
     auto clear_v_rows = [&](int it, int z0, int z1) -> bool {
-      const int st = it % kStages;
+      const int gt = base + it, st = gt % kStages;
       // (With one stage the tile before may not have landed yet: QK(it - 1) says
       // nothing of V(it - 1), only of V(it - 2), and a parity wait one phase early
       // would pass.)
-      if (kStages == 1 && it > 0 &&
-          !mbar_wait(&full_v[0], (uint32_t)(it - 1) & 1u, p.err, abort_flag))
+      if (kStages == 1 && gt > 0 &&
+          !mbar_wait(&full_v[0], (uint32_t)(gt - 1) & 1u, p.err, abort_flag))
         return false;
-      if (!mbar_wait(&full_v[st], (uint32_t)(it / kStages) & 1u, p.err, abort_flag)) return false;
+      if (!mbar_wait(&full_v[st], (uint32_t)(gt / kStages) & 1u, p.err, abort_flag)) return false;
       const int j = kv_tile(it) * kTileN + r;
       if (j < z0 || j >= z1) {
         uint8_t* vt = smem + C::kRing + st * C::kStageBytes + NSTREAM * C::kTile;
@@ -1102,7 +1299,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
     // Multiplies O (and l) by 2^(m_from - m_to) and adopts m_to; O holds
     // P_0..P_{it-1} V, whose MMAs are complete once o_done says so.
     auto rescale_o = [&](int it, bool mine, float m_to) -> bool {
-      const bool o_ok = mbar_wait(&o_done[slot], (uint32_t)(it - 1) & 1u, p.err, abort_flag);
+      const bool o_ok = mbar_wait(&o_done[slot], (uint32_t)(base + it - 1) & 1u, p.err, abort_flag);
       if (!__all_sync(0xffffffffu, o_ok)) return false;
       tc_fence_after();
       const float f = mine ? ex2_approx(m_used - m_to) : 1.f;
@@ -1141,8 +1338,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       mbar_arrive(&p_full[slot]);
     }
     for (int it = 0; ok && !warp_idle && it < n_tiles; ++it) {
-      const int e = it & 1;  // early key half; P of the tile lives in its columns
-      const uint32_t ph = (uint32_t)it & 1u;
+      const int e = (base + it) & 1;  // early key half; P of the tile lives in its columns
+      const uint32_t ph = (uint32_t)(base + it) & 1u;
       const int t_kv = kv_tile(it);
       const bool edge = ((!glob || it < n_band) && !(t_kv >= int_lo && t_kv <= int_hi)) ||
                         (inplace && t_kv * kTileN < gap_hi && t_kv * kTileN + kTileN > gap_lo);
@@ -1166,10 +1363,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       float sv[64];
 
       if constexpr (fixed_ref) {
-        // Exponentials against 0: no maximum to find, none to adopt.  (Both halves
-        // unrolled at D = 128: 160 -> 156 us for 8192 packed tokens; at D = 64 a
-        // loop, 138 against 140 us for a window of 700.)
-#pragma unroll (D == 128 ? 2 : 1)
+        // exponentials against 0: no maximum to find, none to adopt
+#pragma unroll 1
         for (int late = 0; late < 2; ++late) {
           const int hf = e ^ late, pcol = 64 * e + 32 * late;
           const bool w_ok =
@@ -1264,7 +1459,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
             const float m_old = m_used;
             if (late) {
               // O must hold the early half's PV before it is scaled
-              const bool oe_ok = mbar_wait(&oe_done[slot], (uint32_t)it & 1u, p.err, abort_flag);
+              const bool oe_ok = mbar_wait(&oe_done[slot], ph, p.err, abort_flag);
               if (!__all_sync(0xffffffffu, oe_ok)) { ok = false; break; }
             }
             if (!rescale_o(it, jump, m_ref + hmax)) { ok = false; break; }
@@ -1365,7 +1560,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
         const bool jump = tmax1 * sl2 > m_used + 64.f;
         if (__any_sync(0xffffffffu, jump)) {
           const float m_old = m_used;
-          const bool oe_ok = mbar_wait(&oe_done[slot], (uint32_t)it & 1u, p.err, abort_flag);
+          const bool oe_ok = mbar_wait(&oe_done[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, oe_ok)) { ok = false; break; }
           if (!rescale_o(it, jump, fmaxf(m_used, tmax1 * sl2))) { ok = false; break; }
           const float f = jump ? ex2_approx(m_old - m_used) : 1.f;
@@ -1387,7 +1582,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
         if (adopt) m_used = tmax1 * sl2;
         if (__any_sync(0xffffffffu, jump)) {
           const float m_old = m_used;
-          const bool oe_ok = mbar_wait(&oe_done[slot], (uint32_t)it & 1u, p.err, abort_flag);
+          const bool oe_ok = mbar_wait(&oe_done[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, oe_ok)) { ok = false; break; }
           if (!rescale_o(it, jump, fmaxf(m_used, tmax1 * sl2))) { ok = false; break; }
           const float f = jump ? ex2_approx(m_old - m_used) : 1.f;
@@ -1428,7 +1623,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       if (p.lse) p.lse[((size_t)b * p.H + h) * p.N + m_row] = -INFINITY;
     }
     bool fin = ok && n_tiles > 0 && !warp_idle;
-    if (fin) fin = mbar_wait(&o_final[slot], 0, p.err, abort_flag);
+    if (fin) fin = mbar_wait(&o_final[slot], (uint32_t)full & 1u, p.err, abort_flag);
     if (pair) {
       // The two parts of the key walk merge through distributed shared
       // memory.  Once both have finished their MMAs (each tells the other
@@ -1606,10 +1801,24 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
       else if (row_valid && p.lse)
         p.lse[((size_t)b * p.H + h) * (qwin ? Mq : p.N) + (qwin ? m_row : i_phys)] = lse_v;
     }
+    if (chain && __all_sync(0xffffffffu, fin || (ok && n_tiles == 0))) {
+      if (n_tiles > 0) {
+        // O and the whole of S are read out
+        tc_fence_before();
+        mbar_arrive(&o_free[slot]);
+        base += n_tiles;
+        ++full;
+      }
+      if (__all_sync(0xffffffffu, next_item(++n_item))) goto another_item;
+    }
   }
 
   // ---- teardown: make sure no MMA is in flight, then free TMEM.
-  if (warp >= 1 && warp <= NSLOT && lane == 0 && n_tiles > 0 && slot_ok[warp - 1] &&
+  if (chain && warp >= 1 && warp <= NSLOT && lane == 0) {
+    volatile int no_abort = 0;
+    mbar_wait(&mma_done[warp - 1], 0, nullptr, &no_abort, 100000000ull);
+  }
+  if (!chain && warp >= 1 && warp <= NSLOT && lane == 0 && n_tiles > 0 && slot_ok[warp - 1] &&
       *abort_flag) {
     // abort path: o_final was committed after the last MMA this issuer
     // issued; give it a bounded chance to land before TMEM is released.
@@ -1638,9 +1847,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND>::kThreads,
 // checked once per kernel form.
 template <int D, int NSLOT, int NSTREAM, int KIND, int SC>
 bool fwd_regs_fit() {
-  using C = Cfg<D, NSLOT, NSTREAM, KIND>;
+  using C = Cfg<D, NSLOT, NSTREAM, KIND, SC>;
   if (!(NSLOT == 2 || C::kMinBlocks == 2)) return true;
-  const long need = NSLOT == 2 ? 128L * 56 + 256L * 208 : 128L * 56 + 128L * 200;
+  const long need = (C::kChain ? 128L * 80 : 128L * 56) + (NSLOT == 2 ? 256L * 208 : 128L * 200);
   static std::atomic<int> known{0};
   if (known.load(std::memory_order_acquire) == 0) {
     cudaFuncAttributes fa;

@@ -9,7 +9,7 @@ namespace {
 template <int D, int NSLOT, int SC>
 int launch(const SharedArgs& a, int nsplit, float* part_o, float* part_lse,
            cudaStream_t stream) {
-  using C = Cfg<D, NSLOT, 1, 4>;
+  using C = Cfg<D, NSLOT, 1, 4, SC>;
   const auto kernel = swa_fwd_sm100_kernel<D, NSLOT, 1, 4, SC>;
   static std::atomic<unsigned long long> attr{0};
   if (!smem_attr_once(reinterpret_cast<const void*>(kernel), C::kAlloc, attr)) return SWA_ERR_CUDA;

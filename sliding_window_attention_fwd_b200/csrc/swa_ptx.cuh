@@ -121,6 +121,31 @@ __device__ __forceinline__ void drain_copies(uint64_t* bars, int stages, int fir
                 kDrainLimitNs);
 }
 
+// Claims a CTA of this grid that has not been started (launch control): the
+// answer, 16 bytes at shared address `to`, arrives on bar.  None may be asked for
+// after one that found no CTA.
+__device__ __forceinline__ void claim_next_cta(uint32_t to, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(to),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// blockIdx.x of the CTA in the answer, which is now this CTA's to do; -1: none.
+__device__ __forceinline__ int claimed_cta(uint32_t at) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, a;\n\t}"
+      : "=r"(x)
+      : "r"(at)
+      : "memory");
+  return x;
+}
+
 // Named barrier `id` over `count` threads that also ANDs a predicate over
 // them: every participant gets the same result.
 __device__ __forceinline__ bool bar_red_and(int id, int count, bool v) {
@@ -287,6 +312,17 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
+  return d;
+}
+
+// A descriptor joined from its halves where it is used.  In a loop over items the
+// compiler (nvcc 12.9) otherwise kept a descriptor made before the loop without its
+// upper half: Q came out unswizzled.
+__device__ __forceinline__ uint64_t sdesc_fresh(uint64_t desc) {
+  uint64_t d;
+  asm volatile("mov.b64 %0, {%1, %2};"
+               : "=l"(d)
+               : "r"((uint32_t)desc), "r"((uint32_t)(desc >> 32)));
   return d;
 }
 

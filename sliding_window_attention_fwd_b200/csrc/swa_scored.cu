@@ -9,7 +9,7 @@ namespace {
 template <int D, int NSLOT, int SC>
 int launch(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H,
            int Hkv, int N, int L, int R, const ScoreArgs& sc, float scale, cudaStream_t stream) {
-  using C = Cfg<D, NSLOT, 1, 3>;
+  using C = Cfg<D, NSLOT, 1, 3, SC>;
   const auto kernel = swa_fwd_sm100_kernel<D, NSLOT, 1, 3, SC>;
   static std::atomic<unsigned long long> attr{0};
   if (!smem_attr_once(reinterpret_cast<const void*>(kernel), C::kAlloc, attr)) return SWA_ERR_CUDA;

@@ -124,6 +124,18 @@ def test_two_heads_per_cta(swa, D, cap, bias):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 80.0])
+def test_more_items_than_a_wave(swa, D, cap):
+    """Several items per SM, of many lengths and some empty: tiles of padding, single
+    tokens, more documents than lanes."""
+    cu = [[0] + list(range(300, 340)) + [900, 990], [400] * 30 + list(range(401, 413)) + [450],
+          [0] * 20 + list(range(0, 1000, 45))]
+    assert len({len(c) for c in cu}) == 1
+    run(swa, 3, 1000, 32, 8, D, 200, 0, cap, False, cu=cu)
+    run(swa, 2, 1030, 32, 8, D, -1, -1, cap, False, cu=[[0, 513, 1030], [129, 140, 640]])
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_many_key_tiles(swa, D):
     """Packed documents over more key tiles than SMs (their longest walks go first)."""
     cu = [[0, 700, 701, 900, 1390], [130, 131, 131, 500, 1400]]
