@@ -871,11 +871,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
         // The early half's share is issued as soon as its P is written, so
         // after the softmax finishes a tile only a quarter-tile of PV stands
         // between it and the late half of the next tile's S.
-        auto pv_half = [&](int it, bool first, bool early) {
+        auto pv_half = [&](int it, int e, bool first, bool early) {
           const uint64_t dv =
               (chain ? sdesc_fresh(dv0) : dv0) + (uint64_t)(it % kStages) * kStageStep;
           const uint32_t to = tmem + C::kOcol + (uint32_t)D * s;
-          const int e = it & 1;
           const uint32_t tp = tslot + 64u * (uint32_t)e + (early ? 0u : 32u);
           const int kh = early ? e : (e ^ 1);  // key half
 #pragma unroll
@@ -905,8 +904,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
                               abort_flag);
           tc_fence_after();
           if (ok) {
-            qk_half(base, base & 1, &se_full[s]);
-            qk_half(base, (base & 1) ^ 1, &sl_full[s]);
+            // (an item begins with half 0 wherever it runs, so that its bits do not
+            // depend on the items before; the PV before has been issued)
+            qk_half(base, 0, &se_full[s]);
+            qk_half(base, 1, &sl_full[s]);
             tc_commit(&empty_k[base % kStages]);
             if (chain && nt == 1) tc_commit(q_free);
           }
@@ -916,13 +917,13 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
           for (int it = 0; ok && it < nt; ++it) {
             const int gt = base + it, st = gt % kStages;
             const bool more = it + 1 < nt;
-            const int e_next = (gt + 1) & 1;  // early half of tile it + 1
+            const int e_next = (it + 1) & 1;  // early half of tile it + 1
             ok = false;
             // the early half's P is in TMEM: its share of PV goes first
             if (!mbar_wait(&pe_full[s], (uint32_t)gt & 1u, p.err, abort_flag)) break;
             if (!mbar_wait(&full_v[st], (uint32_t)(gt / kStages) & 1u, p.err, abort_flag)) break;
             tc_fence_after();
-            pv_half(gt, it == 0, true);
+            pv_half(gt, it & 1, it == 0, true);
             tc_commit(&oe_done[s]);
             if (more) {
               // the softmax has read the late half of tile it; K of tile it + 1
@@ -936,7 +937,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
             // P of tile it is in TMEM; V of tile it
             if (!mbar_wait(&p_full[s], (uint32_t)gt & 1u, p.err, abort_flag)) break;
             tc_fence_after();
-            pv_half(gt, false, false);
+            pv_half(gt, it & 1, false, false);
             tc_commit(&o_done[s]);
             tc_commit(&empty_v[st]);
             if (more) {
@@ -1338,7 +1339,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
       mbar_arrive(&p_full[slot]);
     }
     for (int it = 0; ok && !warp_idle && it < n_tiles; ++it) {
-      const int e = (base + it) & 1;  // early key half; P of the tile lives in its columns
+      const int e = it & 1;  // early key half; P of the tile lives in its columns
       const uint32_t ph = (uint32_t)(base + it) & 1u;
       const int t_kv = kv_tile(it);
       const bool edge = ((!glob || it < n_band) && !(t_kv >= int_lo && t_kv <= int_hi)) ||

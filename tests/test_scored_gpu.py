@@ -328,3 +328,39 @@ def test_results_belong_to_the_stream_of_the_call(swa):
     assert torch.empty_like(q).data_ptr() == at  # (it was free)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_forwards_of_several_waves_at_once_and_captured(swa, D):
+    """Forwards whose CTAs take several items: in two streams at once, each beside the
+    other's, and replayed from graphs in turn."""
+    st, calls = [torch.cuda.Stream() for _ in range(2)], []
+    for i, (N, cu) in enumerate(((2000, [0, 700, 701, 1900]), (1500, [40, 600, 1500]))):
+        q, k, v, _ = inputs(1, N, 32, 8, D, seed=i)
+        kw = {"win_left": 900, "win_right": 0, "softcap": 30.0 * i,
+              "cu_docs": torch.tensor([cu], dtype=torch.int32, device="cuda")}
+        calls.append((q, k, v, kw))
+    want = [swa.swa_forward_scored(q, k, v, **kw) for q, k, v, kw in calls]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, (q, k, v, kw) in enumerate(calls):
+            outs[i].append(swa.swa_forward_scored(q, k, v, stream=st[i], **kw))
+    graphs = []
+    torch.cuda.synchronize()
+    for i, (q, k, v, kw) in enumerate(calls):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = swa.swa_forward_scored(q, k, v, **kw)
+        graphs.append((graph, got))
+    for _ in range(3):
+        for i, (graph, got) in enumerate(graphs):
+            got.zero_()
+        torch.cuda.synchronize()
+        for i, (graph, got) in enumerate(graphs):
+            with torch.cuda.stream(st[i]):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got, want[i]) for i, (_, got) in enumerate(graphs))
+    assert swa.swa_device_error() == 0
