@@ -71,6 +71,25 @@ def test_scores_past_the_cap(swa, cap, D):
     run(swa, 1, 200, 2, 1, D, -1, 0, cap, False, std=6.0)
 
 
+@pytest.mark.parametrize("cap", [50.0, 51.0])  # with and without a running maximum
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [-1.0, 1.0, 0.0])
+def test_saturated_scores(swa, cap, D, sign):
+    """Every score at the cap: below zero, above it, or some of each."""
+    for H, Hkv, N in ((2, 1, 200), (32, 8, 700)):
+        q, k, v, do = inputs(1, N, H, Hkv, D, std=60.0)
+        if sign:
+            q, k = q.abs(), k.abs() * sign
+        kw = {"win_left": 150, "win_right": 0, "softcap": cap}
+        lse = torch.empty(1, H, N, device="cuda")
+        out = swa.swa_forward_scored(q, k, v, lse=lse, **kw)
+        g = swa.swa_backward_scored(q, k, v, out, do, lse, **kw)
+        torch.cuda.synchronize()
+        ref = R.forward(q, k, v, 150, 0, cap, None, None, None, 0.0, do)
+        R.check({"out": out, "lse": lse, **dict(zip(("dq", "dk", "dv"), g))}, ref,
+                ("out", "lse", "dq", "dk", "dv"))
+
+
 @pytest.mark.parametrize("N", [1, 2, 63, 64, 65, 127, 128, 129, 257, 700])
 def test_lengths(swa, N):
     run(swa, 1, N, 2, 1, 128, -1, 0, 30.0, True)
