@@ -1152,15 +1152,13 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
       }
     };
     // zeros over the V rows of tile it outside [z0, z1) (thread r: row r), so
-    // that whatever lies there, NaN included, adds nothing through P = 0
+    // that whatever lies there, NaN included, adds nothing through P = 0.  After
+    // se_full of the tile: its QK was issued once V of the tile before had landed, so
+    // the stage's barrier is in the phase of this V or just past it (the next needs
+    // the P that this warp still owes), and the parity says which.  Earlier, with
+    // one stage, the barrier may be two phases away, and no wait tells those apart.
     auto clear_v_rows = [&](int it, int z0, int z1) -> bool {
       const int gt = base + it, st = gt % kStages;
-      // (With one stage the tile before may not have landed yet: QK(it - 1) says
-      // nothing of V(it - 1), only of V(it - 2), and a parity wait one phase early
-      // would pass.)
-      if (kStages == 1 && gt > 0 &&
-          !mbar_wait(&full_v[0], (uint32_t)(gt - 1) & 1u, p.err, abort_flag))
-        return false;
       if (!mbar_wait(&full_v[st], (uint32_t)(gt / kStages) & 1u, p.err, abort_flag)) return false;
       const int j = kv_tile(it) * kTileN + r;
       if (j < z0 || j >= z1) {
@@ -1345,13 +1343,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
       const bool edge = ((!glob || it < n_band) && !(t_kv >= int_lo && t_kv <= int_hi)) ||
                         (inplace && t_kv * kTileN < gap_hi && t_kv * kTileN + kTileN > gap_lo);
 
-      if (scored) {
-        // padding rows, and pool rows that no query sees, may hold anything
-        const int z0 = docs ? dt.c0 : seen_lo, z1 = docs ? dt.cn : seen_hi;
-        if (t_kv * kTileN < z0 || t_kv * kTileN + kTileN > z1) {
-          if (!__all_sync(0xffffffffu, clear_v_rows(it, z0, z1))) { ok = false; break; }
-        }
-      }
+      // padding rows, and pool rows that no query sees, may hold anything
+      const int z0 = docs ? dt.c0 : seen_lo, z1 = docs ? dt.cn : seen_hi;
+      const bool v_pad = scored && (t_kv * kTileN < z0 || t_kv * kTileN + kTileN > z1);
 
       // adopt a larger max seen on the previous tile (rare after the start)
       const bool pend = !fixed_ref && m_pend > m_used;
@@ -1372,6 +1366,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
               mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
           tc_fence_after();
+          if (v_pad && !late && !__all_sync(0xffffffffu, clear_v_rows(it, z0, z1))) {
+            ok = false;
+            break;
+          }
           bool none;
           const bool h_edge = half_edge(it, hf, edge, none);
           if (!none) read_half(hf, sv);
@@ -1413,6 +1411,10 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
               mbar_wait(late ? &sl_full[slot] : &se_full[slot], ph, p.err, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
           tc_fence_after();
+          if (v_pad && !late && !__all_sync(0xffffffffu, clear_v_rows(it, z0, z1))) {
+            ok = false;
+            break;
+          }
           // (Windows of 700 / 4096, 64-wide heads, bias alone: 160 / 432 us without
           // the skip of halves that no row sees, 155 / 443 with it; with the cap
           // besides 186 / 503 and 187 / 563; neither: whole tiles 132 / 360, halves
