@@ -196,13 +196,24 @@ __device__ __forceinline__ void shape_chunk(const CapCoefs& c, float scale_log2,
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       m[e & 3] = max3f(m[e & 3], fabsf(raw(e).x), fabsf(raw(e).y));
-    if (!__any_sync(0xffffffffu, max3f(m[0], m[1], fmaxf(m[2], m[3])) > c.small)) {
+    if (!__any_sync(0xffffffffu, max3f(m[0], m[1], fmaxf(m[2], m[3])) > c.vote)) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) t[e] = tanh_small(c, raw(e));
     } else {
+      // (rarely taken, so kept small: four pairs at a time, the chunk turned by as
+      // many in between)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        t[e] = make_float2(tanh_any(c, raw(e).x), tanh_any(c, raw(e).y));
+      for (int e = 0; e < 16; ++e) t[e] = raw(e);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        float2 d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = tanh_any(c, t[e]);
+#pragma unroll
+        for (int e = 0; e < 12; ++e) t[e] = t[e + 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[12 + e] = d[e];
+      }
     }
   }
   const float2 unit = (SC & 1) ? make_float2(c.out, c.out) : make_float2(scale_log2, scale_log2);

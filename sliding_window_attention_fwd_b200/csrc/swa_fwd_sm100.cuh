@@ -1108,48 +1108,65 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], fabsf(sv[60 + e]));
         const float big = max3f(t[0], t[1], fmaxf(t[2], t[3]));
-        q.small = !__any_sync(0xffffffffu, big > p.cap.small);
+        q.small = !__any_sync(0xffffffffu, big > p.cap.vote);
       }
       return q;
     };
-    // Addends of the keys 2e and 2e + 1, for e in order: bias and -m_ref.  Off
-    // the diagonal they are stepped through, afresh every eight pairs, so
-    // that at most seven roundings add up.
-    auto next_addend = [&](const HalfShape& q, int e, auto is_linear, float2& add) {
+    // Addends of the keys 2e and 2e + 1 counted from the half's key `from` (a
+    // multiple of 16), for e in order: bias and -m_ref.  Off the diagonal they are
+    // stepped through, afresh every eight pairs, so that at most seven roundings add
+    // up.
+    auto next_addend = [&](const HalfShape& q, float from, int e, auto is_linear, float2& add) {
+      const float k0 = from + (float)(2 * e), k1 = from + (float)(2 * e + 1);
       if (!bias_on) {
         add = make_float2(q.add, q.add);
       } else if (!decltype(is_linear)::value) {
-        add = make_float2(fmaf(nslope2, fabsf(q.base - (float)(2 * e)), q.add),
-                          fmaf(nslope2, fabsf(q.base - (float)(2 * e + 1)), q.add));
+        add = make_float2(fmaf(nslope2, fabsf(q.base - k0), q.add),
+                          fmaf(nslope2, fabsf(q.base - k1), q.add));
       } else if ((e & 7) == 0) {
-        add.x = fmaf(q.k1, (float)(2 * e), q.add);
-        add.y = fmaf(q.k1, (float)(2 * e + 1), q.add);
+        add.x = fmaf(q.k1, k0, q.add);
+        add.y = fmaf(q.k1, k1, q.add);
       } else {
         add = add2(add, make_float2(2.f * q.k1, 2.f * q.k1));
       }
     };
-    auto shape_pair = [&](float2 s, float2 add, auto is_small) -> float2 {
-      if (!cap_on) return fma2(s, make_float2(sl2, sl2), add);
-      return decltype(is_small)::value ? cap_small(p.cap, s, add) : cap_any(p.cap, s, add);
+    // (without a cap, or with every product in the cubic's range)
+    auto shape_pair = [&](float2 s, float2 add) -> float2 {
+      return cap_on ? cap_small(p.cap, s, add) : fma2(s, make_float2(sl2, sl2), add);
     };
     auto shape_half = [&](const HalfShape& q, float (&sv)[64]) {
-      auto run = [&](auto is_small, auto is_linear) {
+      auto run = [&](auto is_linear) {
         float2 add;
+        if (q.small) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          next_addend(q, e, is_linear, add);
-          const float2 x = shape_pair(make_float2(sv[2 * e], sv[2 * e + 1]), add, is_small);
-          sv[2 * e] = x.x;
-          sv[2 * e + 1] = x.y;
+          for (int e = 0; e < 32; ++e) {
+            next_addend(q, 0.f, e, is_linear, add);
+            const float2 x = shape_pair(make_float2(sv[2 * e], sv[2 * e + 1]), add);
+            sv[2 * e] = x.x;
+            sv[2 * e + 1] = x.y;
+          }
+          return;
+        }
+        // Rarely taken, so kept small: 16 keys at a time, the half turned by as
+        // many in between (unrolled, its 700 instructions cost the usual path 2 %).
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          float done[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            next_addend(q, (float)c, e, is_linear, add);
+            const float2 x = cap_any(p.cap, make_float2(sv[2 * e], sv[2 * e + 1]), add);
+            done[2 * e] = x.x;
+            done[2 * e + 1] = x.y;
+          }
+#pragma unroll
+          for (int j = 0; j < 48; ++j) sv[j] = sv[j + 16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sv[48 + j] = done[j];
         }
       };
-      if (bias_on && q.diag) {
-        if (q.small) run(std::true_type(), std::false_type());
-        else run(std::false_type(), std::false_type());
-      } else {
-        if (q.small) run(std::true_type(), std::true_type());
-        else run(std::false_type(), std::true_type());
-      }
+      if (bias_on && q.diag) run(std::false_type());
+      else run(std::true_type());
     };
     // zeros over the V rows of tile it outside [z0, z1) (thread r: row r), so
     // that whatever lies there, NaN included, adds nothing through P = 0.  After
@@ -1275,8 +1292,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
           const int c = jj * 16 + e;
           float2 xa = make_float2(sv[2 * c], sv[2 * c + 1]);
           if (decltype(raw)::value) {
-            next_addend(q, c, std::true_type(), add);
-            xa = shape_pair(xa, add, std::true_type());
+            next_addend(q, 0.f, c, std::true_type(), add);
+            xa = shape_pair(xa, add);
             sv[2 * c] = xa.x;
             sv[2 * c + 1] = xa.y;
           }

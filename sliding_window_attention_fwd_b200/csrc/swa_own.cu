@@ -468,20 +468,20 @@ __global__ void __launch_bounds__(OwnCfg<D>::kThreads, 2)
           float big = 0.f;
 #pragma unroll
           for (int n = 0; n < kNQ; ++n) big = fmaxf(big, fabsf(__uint_as_float(sv[n])));
-          if (!__any_sync(0xffffffffu, valid && big > p.cap.small)) {
+          auto shape = [&](auto form) {
 #pragma unroll
             for (int n = 0; n < kNQ; n += 2) {
-              const float2 x = cap_small(
-                  p.cap, make_float2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])),
-                  make_float2(nslope2[n] * dist, nslope2[n + 1] * dist));
+              const float2 x =
+                  form(p.cap, make_float2(__uint_as_float(sv[n]), __uint_as_float(sv[n + 1])),
+                       make_float2(nslope2[n] * dist, nslope2[n + 1] * dist));
               xs[n] = x.x;
               xs[n + 1] = x.y;
             }
-          } else {
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n)
-              xs[n] = fmaf(nslope2[n], dist, tanh_any(p.cap, __uint_as_float(sv[n])) * p.cap.out);
-          }
+          };
+          if (!__any_sync(0xffffffffu, valid && big > p.cap.vote))
+            shape([](const CapCoefs& c, float2 s, float2 add) { return cap_small(c, s, add); });
+          else
+            shape([](const CapCoefs& c, float2 s, float2 add) { return cap_any(c, s, add); });
         } else {
 #pragma unroll
           for (int n = 0; n < kNQ; ++n)

@@ -19,64 +19,93 @@
 
 namespace swa {
 
-// The cap in log2 units as a function of the raw product s: cap log2(e)
-// tanh(s ci) with ci = scale / cap.
+// The cap in log2 units as a function of the raw product s: cap log2(e) tanh(u)
+// with u = s ci, ci = scale / cap.
 //
-// For |s ci| <= 1/2 (nearly always, with the caps that models use) it is s
-// times a cubic in s^2: a degree-3 polynomial in z fitted to tanh(sqrt z) /
-// sqrt z on [0, 1/4] by iterated weighted least squares (relative error
-// 5.5e-7), its coefficients scaled on the host: four operations on the FMA
-// pipe, none on MUFU, which the exponentials already fill.  A tanh from MUFU
-// (error 2^-11) would be worth 2 % of a probability at a cap of 50.
+// For |u| <= 1/2 (nearly always, with the caps that models use) it is u times a
+// cubic in u^2: a degree-3 polynomial in z fitted to tanh(sqrt z) / sqrt z on
+// [0, 1/4] by iterated weighted least squares (relative error 5.5e-7).  With
+// ci^k folded into the coefficients on the host that is four operations on the
+// FMA pipe, none on MUFU, which the exponentials already fill.  (Forming u first, a
+// fifth one, took 8192 packed tokens from 157 to 169 us, a training step from
+// 334 to 348.)
+// A tanh from MUFU (error 2^-11) would be worth 2 % of a probability at a cap of
+// 50.
 // Elsewhere tanh u = 1 - 2 / (e^{2u} + 1) for either sign (absolute error
-// about 2e-7, which is what the score of a cap keeps; +-1 for infinite u,
-// NaN for NaN), with two MUFU operations.
+// about 5e-7, a like share of a tanh of at least 0.46; +-1 for infinite u, NaN
+// for NaN), with two MUFU operations.  Nearer to 0 that error would count: the
+// cap multiplies it.  So each score takes the form of its own u, and a warp
+// only skips the second one when none of its scores needs it: a score's bits
+// do not depend on its neighbours'.
+// Where the folded coefficients would leave fp32's range (caps from 1e5 scale
+// on, or below 1e-4 scale) u is formed first: pre = ci and plain coefficients.
+// Then every score goes the way of both forms, which multiplies by pre; with
+// folded coefficients pre is 1, and the bits are the short way's.
 struct CapCoefs {
-  float a0, a1, a2, a3;  // of s^0 .. s^6, in log2 units (the backward's: of tanh itself)
-  float small;           // the cubic's range of |s|
-  float two_ci_log2e;    // 2 ci log2 e
+  float pre;
+  float a0, a1, a2, a3;  // of (s pre)^1, ^3, ^5, ^7, in log2 units (the backward's: of tanh itself)
+  float near;            // the cubic's range of |s|
+  float vote;            // no score beyond it: the short way (-1: never)
+  float far2;            // s pre far2 = 2 u log2 e
   float out;             // cap log2 e (0: no cap)
 };
 
 inline CapCoefs cap_coefs(float softcap, float scale, bool log2_units = true) {
   CapCoefs c{};
   if (!(softcap > 0.f)) return c;
-  const double ci = (double)scale / softcap, co = softcap * 1.4426950408889634;
-  const double z = ci * ci, unit = log2_units ? co : 1.0;
-  c.a0 = (float)(0.99999945577 * ci * unit);
-  c.a1 = (float)(-0.33326318 * z * ci * unit);
-  c.a2 = (float)(0.13190297 * z * z * ci * unit);
-  c.a3 = (float)(-0.04440222 * z * z * z * ci * unit);
-  // (outside this range of ci the scaled coefficients would lose bits)
-  c.small = ci > 1e-5 && ci < 1e4 ? (float)(0.5 / ci) : -1.f;
-  c.two_ci_log2e = (float)(2.0 * ci * 1.4426950408889634);
+  double ci = (double)scale / softcap, co = softcap * 1.4426950408889634;
+  // ci and 1 / ci stay normal fp32 numbers.  A cap beyond 1e30 scale leaves every
+  // product below 1e27 as it is (u^2 / 3 < 2^-24), and so does 1e30 scale in its
+  // place; one below 1e-30 scale makes every product from 1e-29 on the cap itself.
+  if (ci < 1e-30) {
+    ci = 1e-30;
+    co = scale * 1.4426950408889634 / ci;
+  }
+  if (ci > 1e30) ci = 1e30;
+  const bool fold = ci > 1e-5 && ci < 1e4;
+  const double unit = log2_units ? co : 1.0, f = fold ? ci : 1.0, z = f * f;
+  c.pre = fold ? 1.f : (float)ci;
+  c.a0 = (float)(0.99999945577 * f * unit);
+  c.a1 = (float)(-0.33326318 * z * f * unit);
+  c.a2 = (float)(0.13190297 * z * z * f * unit);
+  c.a3 = (float)(-0.04440222 * z * z * z * f * unit);
+  c.near = (float)(0.5 / ci);
+  c.vote = fold ? c.near : -1.f;
+  c.far2 = (float)(2.0 * f * 1.4426950408889634);
   c.out = (float)co;
   return c;
 }
 
-// Capped scores of a pair of products plus add.
-__device__ __forceinline__ float2 cap_small(const CapCoefs& c, float2 s, float2 add) {
+// The cubic of w = (s pre)^2 for a pair.
+__device__ __forceinline__ float2 cap_cubic(const CapCoefs& c, float2 s) {
   const float2 w = mul2(s, s);
   float2 q = fma2(make_float2(c.a3, c.a3), w, make_float2(c.a2, c.a2));
   q = fma2(q, w, make_float2(c.a1, c.a1));
-  q = fma2(q, w, make_float2(c.a0, c.a0));
-  return fma2(s, q, add);
+  return fma2(q, w, make_float2(c.a0, c.a0));
 }
-__device__ __forceinline__ float tanh_any(const CapCoefs& c, float s) {
+__device__ __forceinline__ float tanh_far(const CapCoefs& c, float s) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_approx(s * c.two_ci_log2e) + 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_approx(s * c.far2) + 1.f));
   return fmaf(-2.f, r, 1.f);
 }
-// tanh of a pair (coefficients of tanh itself).
-__device__ __forceinline__ float2 tanh_small(const CapCoefs& c, float2 s) {
-  const float2 w = mul2(s, s);
-  float2 q = fma2(make_float2(c.a3, c.a3), w, make_float2(c.a2, c.a2));
-  q = fma2(q, w, make_float2(c.a1, c.a1));
-  q = fma2(q, w, make_float2(c.a0, c.a0));
-  return mul2(s, q);
+// Capped scores of a pair of products plus add: with every |s| <= vote, or with any.
+__device__ __forceinline__ float2 cap_small(const CapCoefs& c, float2 s, float2 add) {
+  return fma2(s, cap_cubic(c, s), add);
 }
 __device__ __forceinline__ float2 cap_any(const CapCoefs& c, float2 s, float2 add) {
-  return fma2(make_float2(tanh_any(c, s.x), tanh_any(c, s.y)), make_float2(c.out, c.out), add);
+  const float2 v = mul2(s, make_float2(c.pre, c.pre)), near = cap_small(c, v, add);
+  const float2 far = fma2(make_float2(tanh_far(c, v.x), tanh_far(c, v.y)),
+                          make_float2(c.out, c.out), add);
+  return make_float2(fabsf(s.x) <= c.near ? near.x : far.x, fabsf(s.y) <= c.near ? near.y : far.y);
+}
+// tanh of a pair (coefficients of tanh itself), likewise.
+__device__ __forceinline__ float2 tanh_small(const CapCoefs& c, float2 s) {
+  return mul2(s, cap_cubic(c, s));
+}
+__device__ __forceinline__ float2 tanh_any(const CapCoefs& c, float2 s) {
+  const float2 v = mul2(s, make_float2(c.pre, c.pre)), near = tanh_small(c, v);
+  return make_float2(fabsf(s.x) <= c.near ? near.x : tanh_far(c, v.x),
+                     fabsf(s.y) <= c.near ? near.y : tanh_far(c, v.y));
 }
 
 // The documents of one row of tokens.
