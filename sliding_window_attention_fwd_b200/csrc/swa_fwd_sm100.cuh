@@ -1750,8 +1750,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
       tc_fence_after();
       // (l == 0: a part of a split walk with none of the row's keys, whose
       // lse is -inf and which the merge skips, or a padding row: zeros)
-      // (a row without keys: its maximum never rose)
-      const bool none = scored && m_used == -INFINITY;
+      // (a row without keys: nothing was added to its sum.  Its maximum would not say so:
+      // one over NaN scores and masked ones is -inf too.)
+      const bool none = scored && l == 0.f;
       const float inv = l > 0.f && !none ? 1.f / l : 0.f;
       const size_t orow_i = qwin ? (size_t)b * Mq + m_row : (size_t)b * p.N + i_phys;
       uint16_t* orow = p.out + (orow_i * p.H + h) * D;
