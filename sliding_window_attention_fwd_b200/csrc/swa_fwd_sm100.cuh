@@ -1460,7 +1460,9 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
                           make_float2(0.f, 0.f)};
           // the usual half, with no key to mask: P is formed while the half's
           // maximum is found (a row's first against 0, which holds for any
-          // maximum in [-20, 64]); otherwise the maximum comes first
+          // maximum in [-20, 64]); otherwise the maximum comes first (and the
+          // reference is the same: a row's bits do not depend on which way the
+          // other rows of the warp need)
           const bool usual = !q.diag && q.small && !h_edge;
           if (usual) {
             exp_shaped(pcol, sv, lh, q, std::true_type());
@@ -1472,7 +1474,7 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
           tmax = fmaxf(tmax, m_ref + hmax);
           const bool adopt = m_used == -INFINITY;
           const bool jump = !adopt && hmax > 64.f;
-          const bool holds = usual && hmax <= 64.f && hmax >= -20.f;
+          const bool holds = hmax <= 64.f && hmax >= -20.f;
           if (adopt) m_used = holds ? 0.f : hmax;
           const bool redo = __any_sync(0xffffffffu, jump || (adopt && !holds)) || !usual;
           if (__any_sync(0xffffffffu, jump)) {
