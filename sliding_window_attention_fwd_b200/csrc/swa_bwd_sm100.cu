@@ -293,6 +293,14 @@ __device__ __forceinline__ void clear_row(uint8_t* tile, int r, int row0, int z0
         make_uint4(0u, 0u, 0u, 0u);
 }
 
+// failure-detection test build only: the load of this step's streamed tiles (dq: K,
+// dkdv: Q and dO) is never issued, so the MMA issuer's bounded wait for it runs out
+#ifdef SWA_TEST_WITHHOLD_TILE
+constexpr int kWithheld = SWA_TEST_WITHHOLD_TILE;
+#else
+constexpr int kWithheld = -1;
+#endif
+
 // ======================================================== dq kernel
 // kShaped: shaped scores and documents (token-level band, no dilation); SC: 1
 // a cap, 2 a bias, 3 both.
@@ -413,8 +421,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const int t = tr.kv_begin + it;
         uint8_t* kb = smem + C::kRing + st * C::kStageBytes;
         if (it >= S_ && !mbar_wait(&empty_k[st], ph ^ 1u, p.err, abort_flag)) break;
-        mbar_arrive_expect_tx(&full_k[st], C::kTile);
-        load_tile<D>(kb, &p.tmK[map_idx], &full_k[st], p, c, g_kv, t * kTileN, b);
+        if (it != kWithheld) {
+          mbar_arrive_expect_tx(&full_k[st], C::kTile);
+          load_tile<D>(kb, &p.tmK[map_idx], &full_k[st], p, c, g_kv, t * kTileN, b);
+        }
         last_k = it;
         if (it >= S_ && !mbar_wait(&empty_v[st], ph ^ 1u, p.err, abort_flag)) break;
         mbar_arrive_expect_tx(&full_v[st], C::kTile);
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (kShaped && n_tiles == 0) drain_copies(full_q, 1, 0, 0);
       if (*abort_flag) {
         drain_copies(full_q, 1, 0, 0);
-        drain_copies(full_k, S_, 0, last_k);
+        drain_copies(full_k, S_, 0, last_k, kWithheld);
         drain_copies(full_v, S_, 0, last_v);
       }
     }
@@ -695,8 +705,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         }
       }
     } else if (row_valid && n_tiles == 0 && cg == 0) {
-      // no key at all (cannot happen for a valid row: its own key is always
-      // in the window), kept for completeness
+      // a tile of padding rows (a band's rows always see their own key)
       uint4* dst = reinterpret_cast<uint4*>(p.dq + (((size_t)b * p.N + i_phys) * p.H + h) * D);
       for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         load_tile<D>(qb, &p.tmQ[map_idx], &full[st], p, c, h, qt * kTileM, b);
         load_tile<D>(qb + C::kTile, &p.tmDO[map_idx], &full[st], p, c, h, qt * kTileM, b);
       };
-      if (s < S_ && lane == 0) load_rows();
+      if (s < S_ && lane == 0 && s != kWithheld) load_rows();
       // lse (log2 units) and Delta of the tile's 128 query rows, loaded into
       // registers before the wait for the stage so their latency overlaps it;
       // rows past the class end get lse = +inf (P = 0)
@@ -838,7 +847,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
       if (s >= S_) {
         if (!mbar_wait(&empty[st], ph ^ 1u, p.err, abort_flag)) break;
-        if (lane == 0) load_rows();
+        if (lane == 0 && s != kWithheld) load_rows();
       }
       float* vl = vec + st * 2 * kTileM;
 #pragma unroll
@@ -853,7 +862,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     if (kShaped && lane == 0 && n_steps == 0) drain_copies(full_kv, 1, 0, 0);
     if (lane == 0 && *abort_flag) {
       drain_copies(full_kv, 1, 0, 0);
-      drain_copies(full, S_, 0, last);
+      drain_copies(full, S_, 0, last, kWithheld);
     }
   } else if (warp == 1) {
     // ============================== MMA issuer ==============================
