@@ -2,10 +2,12 @@
 from __future__ import annotations
 
 import ctypes
-import importlib
+import importlib.util
 import os
 
 import torch
+
+from . import build as _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libswa.so")
@@ -16,7 +18,6 @@ if not os.path.exists(_LIB_PATH):
         "`python -m sliding_window_attention_fwd_b200.build` (nvcc, sm_100a)")
 
 _lib = ctypes.CDLL(_LIB_PATH)
-_calls = importlib.import_module("._torch_calls", __package__)  # csrc/swa_torch.cpp, built with it
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -101,9 +102,37 @@ class SwaError(RuntimeError):
         super().__init__(f"{where}: {swa_status_string(status)} ({status})")
 
 
-_calls.init(SwaError, *(ctypes.cast(getattr(_lib, _n), _P).value for _n in (
-    "swa_forward_scored", "swa_backward_scored", "swa_rope_append_paged", "swa_decode_shared",
-    "swa_decode_shared_workspace_bytes")))
+class _NoCalls:
+    """Stands for the extension module where it cannot be loaded: the functions that go
+    through it say so, the others work without it."""
+
+    def __init__(self, why: str):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(self.why)
+
+
+def _load_calls():
+    """The extension module of csrc/swa_torch.cpp, handed the library's entry points."""
+    path = _build.calls_path()
+    advice = "build it with `python -m sliding_window_attention_fwd_b200.build`"
+    if not os.path.exists(path):
+        return _NoCalls(f"the binding's extension module for torch {torch.__version__} is "
+                        f"missing ({path}): {advice}")
+    spec = importlib.util.spec_from_file_location(__package__ + "._torch_calls", path)
+    try:
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+    except ImportError as e:
+        return _NoCalls(f"{e}: {advice}")
+    calls.init(SwaError, *(ctypes.cast(getattr(_lib, n), _P).value for n in (
+        "swa_forward_scored", "swa_backward_scored", "swa_rope_append_paged",
+        "swa_decode_shared", "swa_decode_shared_workspace_bytes")))
+    return calls
+
+
+_calls = _load_calls()
 
 
 def library_path() -> str:

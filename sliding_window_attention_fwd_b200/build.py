@@ -5,6 +5,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sysconfig
 import tempfile
@@ -14,7 +15,6 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libswa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 CALLS_SRC = os.path.join(CSRC, "swa_torch.cpp")
-CALLS = os.path.join(HERE, "_torch_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -33,8 +33,25 @@ def deps():
         glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def torch_version() -> str:
+    """The installed torch's version, without importing it."""
+    with open(os.path.join(torch_dir(), "version.py")) as f:
+        return re.search(r"__version__ *= *['\"]([^'\"]+)", f.read()).group(1)
+
+
+def calls_path() -> str:
+    """The extension module.  It is bound to the torch it was built with, so its file
+    bears that version: another torch finds no module instead of a broken one."""
+    return os.path.join(HERE, f"_torch_calls-{torch_version()}.so")
+
+
 def stale() -> bool:
-    for built, needs in ((LIB, deps()), (CALLS, [CALLS_SRC, os.path.join(INCLUDE, "swa.h")])):
+    for built, needs in ((LIB, deps()),
+                         (calls_path(), [CALLS_SRC, os.path.join(INCLUDE, "swa.h")])):
         if not os.path.exists(built):
             return True
         if any(os.path.getmtime(p) > os.path.getmtime(built) for p in needs):
@@ -45,14 +62,14 @@ def stale() -> bool:
 def calls_command():
     """g++ command of the extension module.  torch and its libraries are loaded
     before it is imported, so it carries no path to them."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = torch_dir()
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-            "-isystem", os.path.join(torch_dir, "include"),
-            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-            "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", CALLS,
-            "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", calls_path(),
+            "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_python"]
 
 
