@@ -439,9 +439,15 @@ typedef struct swa_score {
  *   K(i) = [max(ds, i - win_left), min(de - 1, max(i + win_right, pe - 1))],
  *   s_ij = softcap tanh(scale q_i . k_j / softcap) - slopes[h] |i - j|.
  * (win_left, win_right < 0: unbounded.)  Padding rows get out = 0 and lse =
- * -inf; what q, k, v hold there, NaN included, reaches no other row.  score
- * NULL: plain scores.  0 <= softcap <= 1e30.  Any GQA group.  Otherwise as
- * swa_forward; no workspace.
+ * -inf; what q, k, v hold there, NaN included, reaches no other row.  In the
+ * documents q and k may hold NaN or infinities too, which reach the rows that
+ * see them and no other; v has to be finite (documents and the edges of windows
+ * share tiles of 128 keys, where a masked key's v meets a probability of 0).
+ * Probabilities are summed unnormalised in fp32: elements of v from 1e-15 to
+ * 1e16 / (keys of the row) in size, and zeros, lose nothing by that.
+ * score NULL: plain scores.  0 <= softcap <= 1e30; a cap far above the scores
+ * leaves them as they are.  Any GQA group.  Otherwise as swa_forward; no
+ * workspace.
  */
 SWA_API int swa_forward_scored(const void* q, const void* k, const void* v, void* out,
                                float* lse, int B, int H, int Hkv, int N, int D, int win_left,
@@ -455,6 +461,8 @@ SWA_API int swa_forward_scored(const void* q, const void* k, const void* v, void
  *   dS_ij = P_ij (dO_i . v_j - dO_i . out_i) (1 - t_ij^2),
  *   dQ_i = scale sum_j dS_ij k_j,  dK_j = scale sum_i dS_ij q_i.
  * Tensors as for swa_backward; padding rows of dq, dk, dv are written as 0.
+ * What padding holds reaches no gradient; in the documents q, k, v, out and dout
+ * have to be finite, for the reason given above.
  * delta: [B, H, N] fp32 device scratch of the caller (dO . out), overwritten;
  * two calls may run at the same time if theirs differ.  No atomics: the same
  * inputs give the same bits.
@@ -488,7 +496,8 @@ SWA_API int swa_backward_scored(const void* q, const void* k, const void* v, con
  * time if theirs differ.  Nothing is allocated.  D in {64, 128}; H / Hkv <= 8;
  * page_size a multiple of 64; num_pages * page_size < 2^31.  Rows of the pool
  * that no query sees may hold anything, NaN included, but for V between two
- * prefix positions that some queries see.
+ * prefix positions that some queries see; V that is seen has to be finite, with
+ * sizes as for swa_forward_scored.
  */
 SWA_API int swa_decode_shared(const void* q, const void* k_pages, const void* v_pages, void* out,
                               float* lse, const int32_t* prefix_table, int n_prefix,

@@ -523,7 +523,8 @@ def swa_decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, 
     block_table [B, max_pages] int32; keep_prefix: the prefix stays visible
     behind the window W; max_tail: the longest sequence's tokens behind the
     prefix (default: what the block table has room for), which only sets how
-    the work is split.  The workspace comes from torch's allocator.  Returns out
+    the work is split, and splits it badly where the table has room for far
+    more.  The workspace comes from torch's allocator.  Returns out
     [B, H, D]."""
     return _calls.decode_shared(q, k_pages, v_pages, prefix_table, n_prefix, block_table, pos,
                                 page_size, W, out, lse, keep_prefix, max_tail, softcap, slopes,

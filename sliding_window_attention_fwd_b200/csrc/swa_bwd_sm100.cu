@@ -43,9 +43,9 @@
 //   dS_ij = P_ij (dP_ij - Delta_i) (1 - t_ij^2);
 // the walks come from the documents, the dkdv kernel takes the longest first,
 // and it is scheduled beside the dq kernel's last CTAs.  Causal window of 4096
-// at N = 8192, H 32 / Hkv 8, D = 128: 1530 us plain, 1610 with a document table,
-// 1710 capped at 50; bound like the plain form by the latency between a step's
-// MMAs and element-wise work.
+// at N = 8192, H 32 / Hkv 8, D = 128: 1540 to 1610 us plain, 1480 to 1600 with a
+// document table, 1720 to 1800 capped at 50; bound like the plain form by the
+// latency between a step's MMAs and element-wise work.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

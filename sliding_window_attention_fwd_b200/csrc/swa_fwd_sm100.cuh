@@ -43,7 +43,8 @@
 //              that jumps by more than 2^64 at once (the half is redone), and
 //              the final O / l is exact either way.  With two slots the
 //              producer/issuer warpgroup gives registers to the softmax
-//              warpgroups (setmaxnreg), which then run without spills.
+//              warpgroups (setmaxnreg).  (A thread then spills at most 32 bytes,
+//              but 260 to 400 in the forms that go from item to item.)
 // Per row: out = O / l (bf16), lse = m + ln l (fp32).
 //
 // Two more forms share the roles, the pipeline and the tiles:
@@ -51,12 +52,14 @@
 //    of a tile comes from the documents of its rows, and the softmax warps turn
 //    raw products into capped and biased scores before the exponentials.  The
 //    tensor core has to do 4 D operations a pair as before; the cap adds five
-//    operations a score on the FMA pipe, and what bounds the form is the issue
-//    of two softmax warps per sub-partition.  A cap alone bounds the scores, and
-//    the running maximum falls away (kFixedRef).  Causal window of 4096 at N =
-//    8192, H 32 / Hkv 8, D = 128: 375 us plain, 432 with a document table, 435
-//    capped at 50, 460 with a distance bias, 550 with both; with all scores past
-//    half the cap 795 (two more MUFU operations each).
+//    operations a score on the FMA pipe.  Tensor pipe and MUFU stay under half and
+//    1.5 to 1.8 instructions of 4 issue a cycle: what bounds the form is the
+//    latency of each phase of two softmax warps per sub-partition.  A cap alone
+//    bounds the scores, and the running maximum falls away (kFixedRef).  Causal
+//    window of 4096 at N = 8192, H 32 / Hkv 8, D = 128: 375 us plain, 435 to 460
+//    with a document table, 440 to 455 capped at 50, 465 to 480 with a distance
+//    bias, 530 to 560 with both; with many scores past half the cap (a cap of 3)
+//    900 to 920: two more MUFU operations each, and both forms of the cap.
 //  * the shared prefix of a decode (kind 4): the rows of an item are every
 //    sequence's query vectors of one kv head, the keys the prefix's pages, and
 //    the key walk is split until the SMs are full.
@@ -86,8 +89,11 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kRescaleShaped = 32.0f;
 // Scores that a cap holds within this many log2 units of 0 (a cap of 50 is 72.1)
 // need no running maximum: every exponential is taken against 0, and P, l and O
-// stay far inside fp32 (and P in bf16, which has its exponents).  Larger caps take
-// the form with a bias, its slopes zero.
+// stay inside fp32 (and P in bf16, which has its exponents): of its 2^127, 2^73 for P
+// leave 2^54 for the number of keys times the size of V.  That is the choice; a
+// bound of 100 would leave 2^27, too little for a million keys.  Larger caps take
+// the form with a bias, its slopes zero, at the price of one: a cap of
+// 60 takes 525 us instead of 444 for the window above.
 constexpr float kFixedRef = 73.0f;
 struct FwdParams {
   CUtensorMap tmQ[kMaxClasses];
@@ -1279,8 +1285,8 @@ __global__ void __launch_bounds__(Cfg<D, NSLOT, NSTREAM, KIND, SC>::kThreads,
     // The same for shaped scores, whose maximum is already taken off.  raw: sv
     // holds the raw products still (linear bias, cap in its usual range) and
     // is shaped on the way, so that the FMA pipe works on some keys while MUFU
-    // works on others.  (All exponentials go to MUFU: here the issue slots are
-    // scarcer, and 1/8 on the FMA pipe measured no faster.)
+    // works on others.  (All exponentials go to MUFU: 1/8 on the FMA pipe measured no
+    // faster.)
     auto exp_shaped = [&](int pcol, float (&sv)[64], float2 (&ls)[4], const HalfShape& q,
                           auto raw) {
       float2 add;

@@ -315,9 +315,10 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
-// A descriptor joined from its halves where it is used.  In a loop over items the
-// compiler (nvcc 12.9) otherwise kept a descriptor made before the loop without its
-// upper half: Q came out unswizzled.
+// A descriptor joined from its halves where it is used, for issuers that go from item
+// to item.  With descriptors made before that loop and used in it (nvcc 12.9) QK read Q
+// as if it were not swizzled, as a descriptor without its upper half would; joined here
+// the same source is right.  Why is not known.
 __device__ __forceinline__ uint64_t sdesc_fresh(uint64_t desc) {
   uint64_t d;
   asm volatile("mov.b64 %0, {%1, %2};"

@@ -18,8 +18,8 @@
 // two vectors whose elements pair up (or, for the adjacent-pair form, two
 // neighbouring ones), eight angles for either form.
 //
-// Measured: 7564 tokens of 48 heads of 128 (186 MB) 37.5 us, 5.0 TB/s; one
-// token of 64 sequences 4.1 us.  Two and three units in flight per thread, 1,
+// Measured in a captured graph: 7564 tokens of 48 heads of 128 (186 MB) 37.3 us,
+// 5.0 TB/s; one token of 64 sequences 3.8 us.  Two and three units in flight per thread, 1,
 // 2 and 8 tokens a block, 128 to 512 threads and streaming loads and stores
 // took 37 to 51 us for the former.
 #include <cuda_runtime.h>

@@ -117,3 +117,21 @@ def test_decode(swa, cap, D, P, B, bias):
                                 lse=lse, softcap=cap, slopes=sl)
     ref = reference(q, kp, vp, ptab, table, ps, P, 64, 100, True, cap, sl)
     R.check({"out": out, "lse": lse}, ref, ("out", "lse"), f"cap {cap}")
+
+
+@pytest.mark.parametrize("size", [1e-14, 1e13])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("cap", [0.0, 50.0, 51.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_sizes_of_v(swa, size, sign, cap, D):
+    """Small and large values under scores at the cap (far from 0 without one)."""
+    q, k, v, _ = inputs(1, 200, 2, 1, D, 16, std=60.0 if cap else 4.0)
+    q, k, v = q.abs(), k.abs() * sign, (v.double() * size).to(v.dtype)
+    lse = torch.empty(1, 2, 200, device="cuda")
+    # (one document, so that the uncapped call takes the shaped form too)
+    cu = torch.tensor([[0, 200]], dtype=torch.int32, device="cuda")
+    out = swa.swa_forward_scored(q, k, v, lse=lse, win_left=150, win_right=0, softcap=cap,
+                                 cu_docs=cu)
+    ref = R.forward(q, k, v, 150, 0, cap)
+    ref["e_out"] = ref["e_out"] - 1e-30  # (which would be most of a small value's bound)
+    R.check({"out": out, "lse": lse}, ref, ("out", "lse"))

@@ -88,3 +88,23 @@ def test_shared_prefix(swa, cap, bias, D, B):
         got, lse = run(q, k2, keep)
         expect(got, want, bad)
         expect(lse, want_lse, bad)
+
+
+@pytest.mark.parametrize("cap,bias", FORMS)
+@pytest.mark.parametrize("H,Hkv,N,D", [(2, 1, 300, 128), (3, 3, 300, 64), (32, 8, 1300, 128)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_infinities_stay_with_the_rows_that_see_them(swa, cap, bias, H, Hkv, N, D, value):
+    L, cu = 40, [0, 90, 200, N - 5]
+    q, k, v, _ = inputs(1, N, H, Hkv, D, 23)
+    kw = {"win_left": L, "win_right": 0, "softcap": cap, "slopes": slopes_of(H) if bias else None,
+          "cu_docs": torch.tensor([cu], dtype=torch.int32, device="cuda")}
+    want = swa.swa_forward_scored(q, k, v, **kw)
+    hit = torch.zeros(1, N, H, dtype=torch.bool, device="cuda")
+    for j, e in ((10, 90), (100, 200), (230, N - 5)):
+        k[:, j, 0, 3] = value
+        hit[:, j:min(j + L + 1, e), :H // Hkv] = True
+    for i in (60, 150, 285):
+        q[:, i, H - 1, 9] = value
+        hit[:, i, H - 1] = True
+    got = swa.swa_forward_scored(q, k, v, **kw)
+    assert torch.equal(got[~hit], want[~hit])
